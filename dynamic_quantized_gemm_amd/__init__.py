@@ -1,7 +1,9 @@
 """Python binding of libdqip.so: the dynamic quantized inner product,
 QuantizeLinear / DequantizeLinear, the requantizing 1x1 QLinearConv, the
 quantized matrix products, the element-wise quantized operators, the
-general QLinearConv and DynamicQuantizeLSTM on AMD Instinct MI355X (gfx950).
+general QLinearConv, DynamicQuantizeLSTM, and decoding over a paged key-value
+cache (rotary positions, append, attention of one new token, eviction) on AMD
+Instinct MI355X (gfx950).
 
 Argument marshalling only: every step runs in the library's HIP kernels.
 The functions carry the names of the C entry points declared in
@@ -25,5 +27,7 @@ from ._binding import (  # noqa: F401
     DQ_LSTM_BIDIRECTIONAL, DQ_LSTM_FORWARD, DQ_LSTM_HIDDEN_MAX, DQ_LSTM_REVERSE, RNN_ACTIVATIONS,
     dq_lstm_forward, dq_lstm_info, dq_lstm_init, dq_lstm_release, dq_lstm_set_weights,
     lstm_activation_slots, dq_probe_copy, dq_probe_mfma_loop, dqip_forward_noalloc,
-    DQIP_NOALLOC_SCRATCH_BYTES,
+    DQIP_NOALLOC_SCRATCH_BYTES, DQ_ROPE_AXES_MAX, DQ_ROPE_DIM_MAX, dq_rope_forward, dq_rope_info,
+    dq_rope_init, dq_rope_release, DQ_KV_BATCH_MAX, DQ_KV_DIM_MAX, dq_kv_append, dq_kv_attend,
+    dq_kv_evict, dq_kv_info, dq_kv_init, dq_kv_read, dq_kv_release, dq_kv_take_errors,
 )

@@ -23,6 +23,8 @@ DQ_QGEMM_BATCH_RANK_MAX = 8
 DQ_QGEMM_BATCH_MAX = 65536
 DQ_LSTM_FORWARD, DQ_LSTM_REVERSE, DQ_LSTM_BIDIRECTIONAL = 0, 1, 2
 DQ_LSTM_HIDDEN_MAX = 4096
+DQ_ROPE_DIM_MAX, DQ_ROPE_AXES_MAX = 1024, 8
+DQ_KV_DIM_MAX, DQ_KV_BATCH_MAX = 256, 65535
 # dq_rnn_act: ONNX RNN activation name -> (code, takes alpha, default alpha,
 # takes beta, default beta)
 RNN_ACTIVATIONS = {
@@ -100,6 +102,21 @@ _SIGNATURES = {
                                       C.c_void_p, C.c_void_p]),
     "dq_lstm_forward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "dq_rope_init": (C.c_int, [C.POINTER(C.c_void_p), C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_int]),
+    "dq_rope_forward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.c_int, C.c_int64, C.c_int64,
+                                  C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int, C.c_void_p]),
+    "dq_rope_info": (C.c_char_p, [C.c_void_p]),
+    "dq_rope_release": (None, [C.c_void_p]),
+    "dq_kv_init": (C.c_int, [C.POINTER(C.c_void_p)] + [C.c_int] * 10),
+    "dq_kv_append": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                               C.c_int64] + [C.c_void_p] * 8 + [C.c_int64, C.c_int64] + [C.c_void_p] * 4),
+    "dq_kv_read": (C.c_int, [C.c_void_p, C.c_int64] + [C.c_void_p] * 10),
+    "dq_kv_attend": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_int64, C.c_int64] + [C.c_void_p] * 7
+                     + [C.c_float, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_float, C.c_void_p]),
+    "dq_kv_evict": (C.c_int, [C.c_void_p] + [C.c_int] * 4 + [C.c_void_p] * 13),
+    "dq_kv_take_errors": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
+    "dq_kv_info": (C.c_char_p, [C.c_void_p]),
+    "dq_kv_release": (None, [C.c_void_p]),
     "dq_lstm_info": (C.c_char_p, [C.c_void_p]),
     "dq_lstm_release": (None, [C.c_void_p]),
     "dq_qconv_release": (None, [C.c_void_p]),
@@ -788,3 +805,193 @@ def dq_lstm_info(ctx):
 def dq_lstm_release(ctx):
     _LSTM_DIMS.pop(ctx, None)
     load().dq_lstm_release(ctx)
+
+
+# -------------------------------------- rotary positions, paged cache
+
+def _rows(t, what, heads, dim, elem, tokens=None):
+    """(pointer, token stride, head stride) of a [tokens, heads, dim] device
+    tensor whose rows of dim are dense; tokens and heads may be strided."""
+    if t.device.type != "cuda":
+        raise DQError(DQ_ERR_ARG, what, "not a device tensor")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (tokens is not None and shape[0] != tokens):
+        raise DQError(DQ_ERR_ARG, what, f"[{'tokens' if tokens is None else tokens}, {heads}, {dim}] expected, "
+                                        f"got {list(shape)}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and dim > 1:
+        raise DQError(DQ_ERR_ARG, what, "the last dimension must be dense")
+    if t.element_size() != elem:
+        raise DQError(DQ_ERR_ARG, what, f"elements of {elem} bytes expected")
+    return t.data_ptr(), ts, hs
+
+
+# sizes of each context made by dq_rope_init: (head_dim, axes)
+_ROPE_DIMS = {}
+
+
+def dq_rope_init(head_dim, rotary_dim, axis_of_pair, inv_freq, interleaved=False):
+    """axis_of_pair, inv_freq: rotary_dim / 2 values each (sequences on the
+    host). Returns the context handle (an int)."""
+    axis, freq = [int(a) for a in axis_of_pair], [float(f) for f in inv_freq]
+    if 2 * len(axis) != rotary_dim or 2 * len(freq) != rotary_dim:
+        raise DQError(DQ_ERR_ARG, "dq_rope_init", f"{rotary_dim // 2} axes and frequencies expected")
+    aa = (C.c_int32 * max(1, len(axis)))(*axis)
+    fa = (C.c_double * max(1, len(freq)))(*freq)
+    h = C.c_void_p()
+    _check(load().dq_rope_init(C.byref(h), int(head_dim), int(rotary_dim), C.addressof(aa), C.addressof(fa),
+                               int(bool(interleaved))), "dq_rope_init")
+    _ROPE_DIMS[h.value] = (int(head_dim), 1 + max(axis))
+    return h.value
+
+
+_ROPE_TYPES = {"torch.float32": DQ_F32, "torch.bfloat16": DQ_BF16, "torch.float16": DQ_F16}
+
+
+def dq_rope_forward(ctx, x, positions, y, inverse=False, type_=None, stream=None):
+    """x, y: [tokens, heads, head_dim], rows dense, tokens and heads may be
+    strided (y may be x); type_ defaults to x's dtype. positions: int32
+    [axes, tokens] (or [tokens] for one axis)."""
+    w = "dq_rope_forward"
+    if ctx not in _ROPE_DIMS:
+        raise DQError(DQ_ERR_STATE, w, "no context")
+    dim, axes = _ROPE_DIMS[ctx]
+    if type_ is None:
+        type_ = _ROPE_TYPES.get(str(x.dtype))
+        if type_ is None:
+            raise DQError(DQ_ERR_TYPE, w, f"{x.dtype} is not supported")
+    n, heads = int(x.shape[0]), int(x.shape[1]) if len(x.shape) == 3 else -1
+    elem = _ELEM.get(type_, 0)
+    xp, xt, xh = _rows(x, w, heads, dim, elem)
+    yp, yt, yh = _rows(y, w, heads, dim, elem, n)
+    _check(load().dq_rope_forward(ctx, xp, type_, n, heads, xt, xh, _ptr(positions, w, 4 * axes * n), yp, yt, yh,
+                                  1 if inverse else 0, _stream(stream)), w)
+
+
+def dq_rope_info(ctx):
+    r = load().dq_rope_info(ctx)
+    return r.decode() if r else None
+
+
+def dq_rope_release(ctx):
+    _ROPE_DIMS.pop(ctx, None)
+    load().dq_rope_release(ctx)
+
+
+# sizes of each context made by dq_kv_init: (batch, q_heads, kv_heads,
+# head_dim, pages_per_seq, slots of a sequence, bytes of a query element,
+# bytes of the cache, bytes of its scales)
+_KV_DIMS = {}
+
+
+def dq_kv_init(batch, q_heads, kv_heads, head_dim, pages, page_size, pages_per_seq, q_type, cache_type,
+               gather_scores=False):
+    """Returns the context handle (an int)."""
+    h = C.c_void_p()
+    _check(load().dq_kv_init(C.byref(h), int(batch), int(q_heads), int(kv_heads), int(head_dim), int(pages),
+                             int(page_size), int(pages_per_seq), q_type, cache_type, int(bool(gather_scores))),
+           "dq_kv_init")
+    rows = int(pages) * int(kv_heads) * int(page_size)
+    _KV_DIMS[h.value] = (int(batch), int(q_heads), int(kv_heads), int(head_dim), int(pages_per_seq),
+                         int(pages_per_seq) * int(page_size), _ELEM[q_type], rows * int(head_dim) * _ELEM[cache_type],
+                         4 * rows)
+    return h.value
+
+
+def _kv_dims(ctx, what):
+    d = _KV_DIMS.get(ctx)
+    if d is None:
+        raise DQError(DQ_ERR_STATE, what, "no context")
+    return d
+
+
+def _kv_cache(d, what, seqs, block_table, k_cache, v_cache, k_scale, v_scale):
+    return (_ptr(block_table, what, 4 * seqs * d[4]), _ptr(k_cache, what, d[7]), _ptr(v_cache, what, d[7]),
+            _ptr(k_scale, what, d[8]), _ptr(v_scale, what, d[8]))
+
+
+def dq_kv_append(ctx, k, v, index, block_table, k_cache, v_cache, k_scale=None, v_scale=None, seq_ids=None, q=None,
+                 q_out=None, rope=None, positions=None, stream=None):
+    """k, v: [tokens, kv_heads, head_dim] (tokens and heads may be strided),
+    stored at slot index[t] of sequence seq_ids[t] (None: of sequence t); q to
+    q_out [tokens, q_heads, head_dim], rotated with k by the dq_rope_init
+    context `rope` at positions [axes, tokens]."""
+    w = "dq_kv_append"
+    d = _kv_dims(ctx, w)
+    n = int(k.shape[0])
+    kp, kt, kh = _rows(k, w, d[2], d[3], d[6])
+    vp, vt, vh = _rows(v, w, d[2], d[3], d[6], n)
+    qp, qt, qh, op, pp = None, 0, 0, None, None
+    if q is not None:
+        qp, qt, qh = _rows(q, w, d[1], d[3], d[6], n)
+        op = _ptr(q_out, w, n * d[1] * d[3] * d[6])
+    if rope is not None:
+        if rope not in _ROPE_DIMS:
+            raise DQError(DQ_ERR_STATE, w, "no rotary context")
+        pp = _ptr(positions, w, 4 * _ROPE_DIMS[rope][1] * n)
+    elif positions is not None:
+        raise DQError(DQ_ERR_ARG, w, "rope and positions go together")
+    _check(load().dq_kv_append(ctx, n, kp, kt, kh, vp, vt, vh, _ptr(index, w, 4 * n), _ptr(seq_ids, w, 4 * n),
+                               *_kv_cache(d, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
+                               qp, qt, qh, op, rope, pp, _stream(stream)), w)
+
+
+def dq_kv_read(ctx, index, block_table, k_cache, v_cache, k_scale=None, v_scale=None, k_out=None, v_out=None,
+               seq_ids=None, stream=None):
+    """The rows at slot index[t] of sequence seq_ids[t] (None: of sequence t)
+    as values, to k_out and v_out [tokens, kv_heads, head_dim]."""
+    w = "dq_kv_read"
+    d = _kv_dims(ctx, w)
+    n = int(index.numel())
+    size = n * d[2] * d[3] * d[6]
+    _check(load().dq_kv_read(ctx, n, _ptr(index, w, 4 * n), _ptr(seq_ids, w, 4 * n),
+                             *_kv_cache(d, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
+                             _ptr(k_out, w, size), _ptr(v_out, w, size), _stream(stream)), w)
+
+
+def dq_kv_attend(ctx, q, lens, block_table, k_cache, v_cache, k_scale, v_scale, out, sm_scale, lse=None, window=0,
+                 scores=None, scores_out=None, decay=1.0, stream=None):
+    """q: [batch, q_heads, head_dim] (strided as k of dq_kv_append), one token
+    of each sequence; out likewise, dense; lse [batch, q_heads] fp32; scores
+    and scores_out [batch, kv_heads, pages_per_seq * page_size] fp32."""
+    w = "dq_kv_attend"
+    d = _kv_dims(ctx, w)
+    n = int(q.shape[0])
+    qp, qt, qh = _rows(q, w, d[1], d[3], d[6])
+    size = 4 * n * d[2] * d[5]
+    _check(load().dq_kv_attend(ctx, n, qp, qt, qh, _ptr(lens, w, 4 * n),
+                               *_kv_cache(d, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
+                               _ptr(out, w, n * d[1] * d[3] * d[6]), sm_scale, _ptr(lse, w, 4 * n * d[1]), window,
+                               _ptr(scores, w, size), _ptr(scores_out, w, size), decay, _stream(stream)), w)
+
+
+def dq_kv_evict(ctx, budget, lens, newest, scores, order, block_table, k_cache, v_cache, k_scale, v_scale,
+                scores_out, order_out, lens_out, recent=0, sinks=0, stream=None):
+    """scores fp32, order int32 [batch, kv_heads, pages_per_seq * page_size];
+    lens, newest int32 [batch]; the outputs may be their inputs."""
+    w = "dq_kv_evict"
+    d = _kv_dims(ctx, w)
+    n = int(lens.numel())
+    size = 4 * n * d[2] * d[5]
+    _check(load().dq_kv_evict(ctx, n, int(budget), int(recent), int(sinks), _ptr(lens, w, 4 * n),
+                              _ptr(newest, w, 4 * n), _ptr(scores, w, size), _ptr(order, w, size),
+                              *_kv_cache(d, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
+                              _ptr(scores_out, w, size), _ptr(order_out, w, size), _ptr(lens_out, w, 4 * n),
+                              _stream(stream)), w)
+
+
+def dq_kv_take_errors(ctx, stream=None) -> int:
+    """Places that did not exist, met since the last call; synchronizes."""
+    n = C.c_int(0)
+    _check(load().dq_kv_take_errors(ctx, C.addressof(n), _stream(stream)), "dq_kv_take_errors")
+    return int(n.value)
+
+
+def dq_kv_info(ctx):
+    r = load().dq_kv_info(ctx)
+    return r.decode() if r else None
+
+
+def dq_kv_release(ctx):
+    _KV_DIMS.pop(ctx, None)
+    load().dq_kv_release(ctx)

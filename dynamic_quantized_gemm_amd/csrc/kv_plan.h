@@ -1,0 +1,90 @@
+// kv_plan.h -- index arithmetic of the paged key-value cache: where a token's
+// row lies, which elements a rotated pair joins, and how the attention's work
+// is shared out. Plain C++ that both the kernels and a host-compiled check
+// use (no HIP header is needed).
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define DQ_HD __host__ __device__ __forceinline__
+#else
+#define DQ_HD inline
+#endif
+
+namespace dq {
+
+// n / d of 32-bit unsigned numbers for a constant d >= 1 by one multiplication
+// (the round-up form of Granlund & Montgomery, PLDI 1994).
+struct KvDiv {
+    uint32_t d, m, s;
+};
+
+inline KvDiv make_kvdiv(uint32_t d) {
+    KvDiv f;
+    f.d = d;
+    f.s = 0;
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << 32) * ((1ull << f.s) - d)) / d + 1);
+    return f;
+}
+
+DQ_HD uint32_t kv_div(uint32_t n, const KvDiv& f) {
+    const uint64_t hi = ((uint64_t)n * f.m) >> 32;
+    return (uint32_t)((hi + n) >> f.s);
+}
+
+// The part of a cache that an index needs: `pages` pages of `page.d` slots for
+// each of `heads` key-value heads, `per_seq` block table entries a sequence.
+struct KvGeom {
+    KvDiv page;
+    int pages, per_seq, heads;
+};
+
+// Row (of D values) of token t of a sequence for key-value head h, where table
+// is the sequence's line of the block table; -1 where t lies beyond the table
+// or its entry names no page. The largest row fits 31 bits (checked when a
+// context is made); byte offsets are taken from it in 64 bits.
+DQ_HD int32_t kv_row(const int32_t* table, uint32_t t, int h, const KvGeom& g) {
+    const uint32_t e = kv_div(t, g.page);
+    if (e >= (uint32_t)g.per_seq) return -1;
+    const uint32_t p = (uint32_t)table[e];
+    if (p >= (uint32_t)g.pages) return -1;
+    return (int32_t)((p * (uint32_t)g.heads + (uint32_t)h) * g.page.d + (t - e * g.page.d));
+}
+
+// The two elements of virtual pair i of a row of D elements, the first R of
+// which are rotated: pairs below R/2 are the rotated ones (halves apart, or
+// neighbours), the others join what passes through unchanged.
+DQ_HD void kv_pair(int i, int D, int R, bool interleaved, int* a, int* b) {
+    if (interleaved) {
+        *a = 2 * i;
+        *b = 2 * i + 1;
+    } else if (i < R / 2) {
+        *a = i;
+        *b = i + R / 2;
+    } else {
+        *a = R + (i - R / 2);
+        *b = *a + (D - R) / 2;
+    }
+}
+
+// ------------------------------------------------------- sharing out tokens
+//
+// The attention's tokens are cut into units of kKvUnit tokens of one sequence
+// and one head tile. Units are numbered sequence by sequence, head tile by
+// head tile; worker w of W takes units [kv_first(w), kv_first(w + 1)), so all
+// have the same number of units to within one, whatever the lengths.
+constexpr int kKvUnit = 128;
+
+DQ_HD int kv_first_token(int len, int window) { return window > 0 && len > window ? len - window : 0; }
+DQ_HD int kv_units(int len, int window) {
+    return (len - kv_first_token(len, window) + kKvUnit - 1) / kKvUnit;
+}
+DQ_HD int64_t kv_first(int w, int W, int64_t units) { return units * w / W; }
+// The worker that takes unit u: the largest w with kv_first(w) <= u.
+DQ_HD int kv_worker(int64_t u, int W, int64_t units) {
+    return (int)(((u + 1) * W - 1) / units);
+}
+
+}  // namespace dq

@@ -1,0 +1,144 @@
+// paged_kv.h -- what the translation units of the paged key-value cache share:
+// the contexts, element types and the angle of a rotary position.
+#pragma once
+
+#include "dq_device.h"
+#include "kv_plan.h"
+
+// Rotary positions: for every pair of the rotated part its position axis and
+// its frequency in turns, inv_freq / 2 pi, as a double and its remainder.
+struct dq_rope_ctx {
+    int device = 0;
+    int D = 0, R = 0, axes = 1, interleaved = 0;
+    double2* freq = nullptr;  // [R / 2] (hi, lo)
+    int32_t* axis = nullptr;  // [R / 2]
+    char info[192] = "";
+};
+
+struct dq_kv_ctx {
+    int device = 0;
+    int batch = 0, Hq = 0, Hk = 0, D = 0, pages = 0, page_size = 0, per_seq = 0, cap = 0;
+    dq_dtype q_type = DQ_BF16, cache_type = DQ_BF16;
+    bool scores = false;
+    dq::KvGeom geom{};
+    int cus = 0;
+    int32_t* bad = nullptr;    // [1] entries that named no page, sequence or length
+    int32_t* moves = nullptr;  // eviction: [batch * Hk] counts, then per head the slots
+                               // freed and those moved into them
+    size_t moves_stride = 0;
+    float* s = nullptr;        // [batch * Hq, s_stride] scores of the attention (log2)
+    size_t s_stride = 0;
+    float* part = nullptr;     // partial results of the attention
+    size_t part_floats = 0;
+    char info[192] = "";
+};
+
+int dq_kv_check_device(const dq_kv_ctx* c);
+int dq_rope_check_device(const dq_rope_ctx* c);
+
+// Attention (paged_attend.hip); the arguments have been checked.
+struct DqAttendArgs {
+    const void* q;
+    long long q_ts, q_hs;  // strides in elements
+    const int32_t* lens;
+    const int32_t* table;
+    const void* k;
+    const void* v;
+    const float* ks;
+    const float* vs;
+    void* out;
+    float* lse;  // may be NULL
+    int batch;
+    float sm_scale;
+    int window;
+    const float* scores;  // NULL: not gathered
+    float* scores_out;
+    float decay;
+};
+size_t dq_attend_part_floats(const dq_kv_ctx* c);
+int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s);
+
+namespace dq {
+
+inline size_t kv_elem_bytes(dq_dtype t) { return t == DQ_F32 ? 4 : t == DQ_I8 ? 1 : 2; }
+
+// Storage of an element type and its conversions (round to nearest even).
+template <int TYPE> struct Elem;
+template <> struct Elem<DQ_F32> { typedef float S; };
+template <> struct Elem<DQ_BF16> { typedef __bf16 S; };
+template <> struct Elem<DQ_F16> { typedef _Float16 S; };
+template <> struct Elem<DQ_I8> { typedef int8_t S; };
+
+// N elements of type S moved as one aligned access where N * sizeof(S) is a
+// power of two up to 16 bytes.
+template <typename S, int N>
+__device__ __forceinline__ void load_vec(const S* p, float (&f)[N]) {
+    typedef S V __attribute__((ext_vector_type(N)));
+    const V v = *(const V*)p;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = (float)v[i];
+}
+template <typename S>
+__device__ __forceinline__ void load_vec(const S* p, float (&f)[1]) { f[0] = (float)*p; }
+
+template <typename S, int N>
+__device__ __forceinline__ void store_vec(S* p, const float (&f)[N]) {
+    typedef S V __attribute__((ext_vector_type(N)));
+    V v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = (S)f[i];
+    *(V*)p = v;
+}
+template <typename S>
+__device__ __forceinline__ void store_vec(S* p, const float (&f)[1]) { *p = (S)f[0]; }
+
+// Element i of a tensor whose type is known at run time.
+__device__ __forceinline__ float load_any(const void* p, int type, long long i) {
+    if (type == DQ_F32) return ((const float*)p)[i];
+    if (type == DQ_BF16) return (float)((const __bf16*)p)[i];
+    if (type == DQ_F16) return (float)((const _Float16*)p)[i];
+    return (float)((const int8_t*)p)[i];
+}
+__device__ __forceinline__ void store_any(void* p, int type, long long i, float f) {
+    if (type == DQ_F32) ((float*)p)[i] = f;
+    else if (type == DQ_BF16) ((__bf16*)p)[i] = (__bf16)f;
+    else ((_Float16*)p)[i] = (_Float16)f;
+}
+
+// cos and sin of pos * freq (freq in turns, hi + lo). The product is reduced
+// to a fraction of a turn in fp64 with its remainder kept, so a position of 31
+// bits loses nothing, and the Taylor series on [-pi/4, pi/4] (first term left
+// out: x^17 / 17! < 5e-17) are summed in fp64, whose rate on this chip is
+// fp32's: the results are fp32 values rounded once. One angle serves every
+// head of a token, so its ~40 operations do not count against the traffic.
+__device__ __forceinline__ void rope_cos_sin(int pos, double2 freq, float* c, float* s) {
+    const double t = (double)pos;
+    const double n = __builtin_rint(t * freq.x);
+    const double r = __builtin_fma(t, freq.y, __builtin_fma(t, freq.x, -n));
+    const double k = __builtin_rint(4.0 * r);
+    const double x = (r - 0.25 * k) * 6.283185307179586476925;
+    const double x2 = x * x;
+    double a = -1.0 / 1307674368000.0;  // -1/15!
+    a = __builtin_fma(a, x2, 1.0 / 6227020800.0);
+    a = __builtin_fma(a, x2, -1.0 / 39916800.0);
+    a = __builtin_fma(a, x2, 1.0 / 362880.0);
+    a = __builtin_fma(a, x2, -1.0 / 5040.0);
+    a = __builtin_fma(a, x2, 1.0 / 120.0);
+    a = __builtin_fma(a, x2, -1.0 / 6.0);
+    a = __builtin_fma(a * x2, x, x);
+    double b = 1.0 / 20922789888000.0;  // 1/16!
+    b = __builtin_fma(b, x2, -1.0 / 87178291200.0);
+    b = __builtin_fma(b, x2, 1.0 / 479001600.0);
+    b = __builtin_fma(b, x2, -1.0 / 3628800.0);
+    b = __builtin_fma(b, x2, 1.0 / 40320.0);
+    b = __builtin_fma(b, x2, -1.0 / 720.0);
+    b = __builtin_fma(b, x2, 1.0 / 24.0);
+    b = __builtin_fma(b, x2, -0.5);
+    b = __builtin_fma(b, x2, 1.0);
+    const int q = (int)k & 3;
+    const double cc = (q & 1) ? a : b, ss = (q & 1) ? b : a;
+    *c = (float)((q == 1 || q == 2) ? -cc : cc);
+    *s = (float)((q & 2) ? -ss : ss);
+}
+
+}  // namespace dq

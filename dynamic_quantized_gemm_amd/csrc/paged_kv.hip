@@ -1,0 +1,767 @@
+// paged_kv.hip -- the paged key-value cache: its context, the append of new
+// keys and values (rotated, and quantized per row for an int8 cache), the read
+// of stored rows, and the eviction of the tokens with the least gathered
+// attention. The attention itself is in paged_attend.hip.
+//
+// The cache is [pages, Hk, page_size, D]: one head's slots of a page are one
+// run of memory, so a head's tokens stream in runs of page_size rows. An int8
+// row's scale is one fp32 of [pages, Hk, page_size].
+#include <math.h>
+#include <stdio.h>
+
+#include <algorithm>
+#include <new>
+
+#include "paged_kv.h"
+
+using namespace dq;
+
+namespace {
+
+// ------------------------------------------------------------------ append
+//
+// A row is one head's D values of one token: the query heads (rotated into
+// q_out), the key heads (rotated, then stored) and the value heads (stored).
+// Sixteen lanes hold a row, in virtual pairs (kv_pair), and walk `chunk` rows
+// of one token with the same cosines and sines. For an int8 cache the row's
+// largest magnitude is reduced over those sixteen lanes in registers, so each
+// row is read once and its codes and scale written once.
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    void* q_out;
+    long long qt, qh, kt, kh, vt, vh;  // strides in elements
+    const int32_t* index;
+    const int32_t* seq_ids;  // NULL: token t belongs to sequence t
+    const int32_t* table;
+    void *kc, *vc;
+    float *ks, *vs;
+    int32_t* bad;
+    const int32_t* pos;  // NULL: no rotation
+    const double2* freq;
+    const int32_t* axis;
+    long long groups;  // tokens * chunks
+    int tokens, batch, Hq, Hk, D, R, chunk;
+    KvDiv chunks;
+    KvGeom geom;
+};
+
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppXor1, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppXor2, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppRowHalfMirror, 0xF, 0xF, false));
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppRowMirror, 0xF, 0xF, false));
+}
+
+template <typename S, int VP, bool IL>
+__device__ __forceinline__ void load_pairs(const S* row, int lo, int hi, float (&a)[VP], float (&b)[VP]) {
+    if constexpr (IL) {
+        float e[2 * VP];
+        load_vec(row + lo, e);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            a[i] = e[2 * i];
+            b[i] = e[2 * i + 1];
+        }
+    } else {
+        load_vec(row + lo, a);
+        load_vec(row + hi, b);
+    }
+}
+
+template <typename S, int VP, bool IL>
+__device__ __forceinline__ void store_pairs(S* row, int lo, int hi, const float (&a)[VP], const float (&b)[VP]) {
+    if constexpr (IL) {
+        float e[2 * VP];
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            e[2 * i] = a[i];
+            e[2 * i + 1] = b[i];
+        }
+        store_vec(row + lo, e);
+    } else {
+        store_vec(row + lo, a);
+        store_vec(row + hi, b);
+    }
+}
+
+constexpr int kKvDimMax = 256;  // 128 pairs: eight a lane
+
+template <int TI, int TC, int VP, bool IL>
+__global__ void __launch_bounds__(256) k_kv_append(const AppendArgs A) {
+    typedef typename Elem<TI>::S SI;
+    typedef typename Elem<TC>::S SC;
+    constexpr int NIT = kKvDimMax / 2 / 16 / VP;
+    const int l = threadIdx.x & 15;
+    const long long g = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+    if (g >= A.groups) return;
+    const uint32_t t = kv_div((uint32_t)g, A.chunks);
+    const int rows = A.Hq + 2 * A.Hk;
+    const int r0 = (int)((uint32_t)g - t * A.chunks.d) * A.chunk, r1 = min(rows, r0 + A.chunk);
+    const int pairs = A.D / 2;
+    const int turned = A.pos ? A.R / 2 : 0;
+
+    float c[NIT][VP], s[NIT][VP];
+    int lo[NIT], hi[NIT];
+    const bool rotate = A.pos && r0 < A.Hq + A.Hk;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+        const int i0 = (it * 16 + l) * VP;
+        kv_pair(i0, A.D, turned ? A.R : A.D, IL, &lo[it], &hi[it]);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            c[it][i] = 1.0f;
+            s[it][i] = 0.0f;
+            if (rotate && i0 < turned)
+                rope_cos_sin(A.pos[(size_t)A.axis[i0 + i] * A.tokens + t], A.freq[i0 + i], &c[it][i], &s[it][i]);
+        }
+    }
+    // where this token goes
+    const int at = r1 > A.Hq ? A.index[t] : -1;
+    const int seq = at < 0 ? 0 : A.seq_ids ? A.seq_ids[t] : (int)t;
+    const bool seq_ok = (uint32_t)seq < (uint32_t)A.batch;
+    const int32_t* line = A.table + (size_t)(seq_ok ? seq : 0) * A.geom.per_seq;
+
+    for (int r = r0; r < r1; ++r) {
+        const bool is_q = r < A.Hq, is_v = r >= A.Hq + A.Hk;
+        const int h = is_q ? r : is_v ? r - A.Hq - A.Hk : r - A.Hq;
+        int32_t row = -1;
+        if (!is_q) {
+            if (at < 0) continue;
+            row = seq_ok ? kv_row(line, (uint32_t)at, h, A.geom) : -1;
+            if (row < 0) {
+                if (l == 0) atomicAdd(A.bad, 1);
+                continue;
+            }
+        }
+        const SI* x = is_q ? (const SI*)A.q + t * A.qt + h * A.qh
+                           : is_v ? (const SI*)A.v + t * A.vt + h * A.vh : (const SI*)A.k + t * A.kt + h * A.kh;
+        float a[NIT][VP], b[NIT][VP];
+        uint32_t top = 0;
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+            const int i0 = (it * 16 + l) * VP;
+            if (i0 >= pairs) continue;
+            load_pairs<SI, VP, IL>(x, lo[it], hi[it], a[it], b[it]);
+            if (!is_v && i0 < turned) {
+#pragma unroll
+                for (int i = 0; i < VP; ++i) {
+                    const float u = a[it][i] * c[it][i] - b[it][i] * s[it][i];
+                    b[it][i] = b[it][i] * c[it][i] + a[it][i] * s[it][i];
+                    a[it][i] = u;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
+                top = max(top, max(__float_as_uint(a[it][i]) & 0x7fffffffu, __float_as_uint(b[it][i]) & 0x7fffffffu));
+        }
+        if (is_q) {
+            SI* y = (SI*)A.q_out + ((size_t)t * A.Hq + h) * A.D;
+#pragma unroll
+            for (int it = 0; it < NIT; ++it)
+                if ((it * 16 + l) * VP < pairs) store_pairs<SI, VP, IL>(y, lo[it], hi[it], a[it], b[it]);
+            continue;
+        }
+        SC* y = (SC*)(is_v ? A.vc : A.kc) + (size_t)row * A.D;
+        if constexpr (TC == DQ_I8) {
+            // magnitudes as integers keep a NaN above infinity: a row that is
+            // not finite is stored as zeros with a NaN for its scale, so that
+            // it reads back as NaN
+            top = max16(top);
+            const bool finite = top < 0x7f800000u;
+            float scale = __uint_as_float(top) / 127.0f;
+            if (!(scale > 0.0f)) scale = 1.0f;
+            const QDiv d = make_qdiv(scale);
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+                if ((it * 16 + l) * VP >= pairs) continue;
+#pragma unroll
+                for (int i = 0; i < VP; ++i) {
+                    a[it][i] = finite ? fminf(fmaxf(rne(qdiv(a[it][i], d)), -127.0f), 127.0f) : 0.0f;
+                    b[it][i] = finite ? fminf(fmaxf(rne(qdiv(b[it][i], d)), -127.0f), 127.0f) : 0.0f;
+                }
+                store_pairs<SC, VP, IL>(y, lo[it], hi[it], a[it], b[it]);
+            }
+            if (l == 0) (is_v ? A.vs : A.ks)[row] = finite ? scale : __uint_as_float(0x7fc00000u);
+        } else {
+#pragma unroll
+            for (int it = 0; it < NIT; ++it)
+                if ((it * 16 + l) * VP < pairs) store_pairs<SC, VP, IL>(y, lo[it], hi[it], a[it], b[it]);
+        }
+    }
+}
+
+// -------------------------------------------------------------------- read
+
+struct ReadArgs {
+    const int32_t* index;
+    const int32_t* seq_ids;
+    const int32_t* table;
+    const void *kc, *vc;
+    const float *ks, *vs;
+    void *k_out, *v_out;
+    int32_t* bad;
+    uint32_t threads;  // tokens * heads * D / 8
+    int Hk, D, batch;
+    KvDiv pieces, heads;
+    KvGeom geom;
+};
+
+// eight values of one row a thread; a slot that holds nothing (index < 0)
+// reads as zeros, one that cannot exist as NaN
+template <int TO, int TC>
+__global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
+    typedef typename Elem<TO>::S SO;
+    typedef typename Elem<TC>::S SC;
+    const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+    if (id >= A.threads) return;
+    const uint32_t rest = kv_div(id, A.pieces);
+    const int e = (int)(id - rest * A.pieces.d) * 8;
+    const uint32_t t = kv_div(rest, A.heads);
+    const int h = (int)(rest - t * A.heads.d);
+    const int at = A.index[t], seq = A.seq_ids ? A.seq_ids[t] : (int)t;
+    int32_t row = -1;
+    if (at >= 0) {
+        if ((uint32_t)seq < (uint32_t)A.batch)
+            row = kv_row(A.table + (size_t)seq * A.geom.per_seq, (uint32_t)at, h, A.geom);
+        if (row < 0 && e == 0) atomicAdd(A.bad, 1);
+    }
+    const size_t o = ((size_t)t * A.Hk + h) * A.D + e;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        SO* out = (SO*)(w ? A.v_out : A.k_out);
+        if (!out) continue;
+        float f[8];
+        if (row < 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = at < 0 ? 0.0f : __uint_as_float(0x7fc00000u);
+        } else {
+            load_vec((const SC*)(w ? A.vc : A.kc) + (size_t)row * A.D + e, f);
+            if constexpr (TC == DQ_I8) {
+                const float scale = (w ? A.vs : A.ks)[row];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= scale;
+            }
+        }
+        if constexpr (TO == DQ_F32) {
+            const float f0[4] = {f[0], f[1], f[2], f[3]}, f1[4] = {f[4], f[5], f[6], f[7]};
+            store_vec(out + o, f0);
+            store_vec(out + o + 4, f1);
+        } else {
+            store_vec(out + o, f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- eviction
+//
+// Of a head's n > budget tokens those with the `budget` largest keys stay,
+// where a key is the gathered weight as an ordered integer, the largest there
+// is for the first `sinks` and last `recent` tokens, ties going to the lowest
+// slot. One workgroup selects for one head: the budget-th largest key digit
+// by digit from histograms in LDS, then the slots below the budget that came
+// free and the slots beyond it that stay, in order, as two lists. A second
+// launch moves the rows, which are most of the traffic, with the whole chip.
+
+struct EvictArgs {
+    const int32_t *lens, *newest;
+    const float* scores;
+    const int32_t* order;
+    const int32_t* table;
+    void *kc, *vc;
+    float *ks, *vs;
+    float* scores_out;
+    int32_t* order_out;
+    int32_t* lens_out;
+    int32_t* moves;
+    size_t moves_stride;
+    int32_t* bad;
+    int batch, Hk, cap, budget, sinks, recent, row_bytes;
+    KvGeom geom;
+};
+
+constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+
+__device__ __forceinline__ uint32_t evict_key(float score, int order, int sinks, long long recent_from) {
+    if (order < sinks || order > recent_from) score = __builtin_inff();
+    const uint32_t k = f2ord(score);
+    return score != score ? 0xffffffffu : k;  // a NaN is the largest
+}
+
+__global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs A) {
+    __shared__ uint32_t hist[256];
+    __shared__ uint32_t wave_a[kSelWaves], wave_b[kSelWaves];
+    __shared__ uint32_t sh_prefix, sh_left;
+    const int item = blockIdx.x, b = item / A.Hk;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int n = A.lens[b];
+    if (n < 0 || n > A.cap) {
+        if (tid == 0 && item % A.Hk == 0) atomicAdd(A.bad, 1);
+        n = n < 0 ? 0 : A.cap;
+    }
+    const size_t base = (size_t)item * A.cap;
+    const float* sc = A.scores + base;
+    const int32_t* od = A.order + base;
+    float* sco = A.scores_out + base;
+    int32_t* odo = A.order_out + base;
+    int32_t* count = A.moves + item;
+    if (n <= A.budget) {
+        for (int i = tid; i < n; i += kSelThreads) {
+            sco[i] = sc[i];
+            odo[i] = od[i];
+        }
+        if (tid == 0) *count = 0;
+        return;
+    }
+    const long long recent_from = (long long)A.newest[b] - A.recent;
+    uint32_t prefix = 0, left = (uint32_t)A.budget;  // keys still to be found below the prefix's ties
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        if (tid < 256) hist[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kSelThreads) {
+            const uint32_t k = evict_key(sc[i], od[i], A.sinks, recent_from);
+            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        }
+        __syncthreads();
+        if (tid == 0) {
+            uint32_t seen = 0;
+            int d = 255;
+            while (d > 0 && seen + hist[d] < left) seen += hist[d--];
+            sh_prefix = prefix | ((uint32_t)d << shift);
+            sh_left = left - seen;
+        }
+        __syncthreads();
+        prefix = sh_prefix;
+        left = sh_left;
+    }
+    // kept: key > prefix, or key == prefix among the first `left` such slots.
+    // A wave takes a run of whole 64s, so that ballots count in slot order.
+    const int run = (n + kSelWaves * 64 - 1) / (kSelWaves * 64) * 64;
+    const int i0 = wave * run, i1 = min(n, i0 + run);
+    const unsigned long long below = (1ull << lane) - 1;
+    uint32_t ties = 0;
+    for (int i = i0 + lane; i - lane < i1; i += 64) {
+        const bool tie = i < i1 && evict_key(sc[i], od[i], A.sinks, recent_from) == prefix;
+        ties += __popcll(__ballot(tie));
+    }
+    if (lane == 0) wave_a[wave] = ties;
+    __syncthreads();
+    uint32_t tie0 = 0;
+    for (int w = 0; w < wave; ++w) tie0 += wave_a[w];
+    __syncthreads();
+    uint32_t holes = 0, movers = 0, t = tie0;
+    for (int i = i0 + lane; i - lane < i1; i += 64) {
+        const uint32_t k = i < i1 ? evict_key(sc[i], od[i], A.sinks, recent_from) : 0;
+        const unsigned long long eq = __ballot(i < i1 && k == prefix);
+        const bool kept = i < i1 && (k > prefix || (k == prefix && t + __popcll(eq & below) < left));
+        t += __popcll(eq);
+        holes += __popcll(__ballot(i < i1 && i < A.budget && !kept));
+        movers += __popcll(__ballot(kept && i >= A.budget));
+    }
+    if (lane == 0) {
+        wave_a[wave] = holes;
+        wave_b[wave] = movers;
+    }
+    __syncthreads();
+    uint32_t hole0 = 0, mover0 = 0, total = 0;
+    for (int w = 0; w < kSelWaves; ++w) {
+        if (w < wave) {
+            hole0 += wave_a[w];
+            mover0 += wave_b[w];
+        }
+        total += wave_a[w];
+    }
+    int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
+    int32_t* src = dst + A.moves_stride;
+    t = tie0;
+    for (int i = i0 + lane; i - lane < i1; i += 64) {
+        const uint32_t k = i < i1 ? evict_key(sc[i], od[i], A.sinks, recent_from) : 0;
+        const unsigned long long eq = __ballot(i < i1 && k == prefix);
+        const bool kept = i < i1 && (k > prefix || (k == prefix && t + __popcll(eq & below) < left));
+        t += __popcll(eq);
+        const bool hole = i < i1 && i < A.budget && !kept, mover = kept && i >= A.budget;
+        const unsigned long long hb = __ballot(hole), mb = __ballot(mover);
+        if (hole) dst[hole0 + __popcll(hb & below)] = i;
+        if (mover) src[mover0 + __popcll(mb & below)] = i;
+        hole0 += __popcll(hb);
+        mover0 += __popcll(mb);
+        if (kept && i < A.budget && sco != sc) sco[i] = sc[i];
+        if (kept && i < A.budget && odo != od) odo[i] = od[i];
+    }
+    if (tid == 0) *count = (int32_t)total;
+    __syncthreads();
+    for (uint32_t m = tid; m < total; m += kSelThreads) {
+        sco[dst[m]] = sc[src[m]];
+        odo[dst[m]] = od[src[m]];
+    }
+}
+
+// rows of keys and values from src to dst slots: sixteen lanes a row, sixteen
+// rows of both a workgroup
+__global__ void __launch_bounds__(256) k_kv_evict_move(const EvictArgs A) {
+    const int item = blockIdx.y, b = item / A.Hk, h = item - b * A.Hk;
+    const int count = A.moves[item];
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
+        const int n = A.lens[b];
+        A.lens_out[b] = n < 0 ? 0 : min(min(n, A.cap), A.budget);
+    }
+    const int l = threadIdx.x & 15;
+    const int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
+    const int32_t* src = dst + A.moves_stride;
+    const int32_t* line = A.table + (size_t)b * A.geom.per_seq;
+    for (int m = blockIdx.x * 16 + (threadIdx.x >> 4); m < count; m += gridDim.x * 16) {
+        const int32_t to = kv_row(line, (uint32_t)dst[m], h, A.geom), from = kv_row(line, (uint32_t)src[m], h, A.geom);
+        if (to < 0 || from < 0) {
+            if (l == 0) atomicAdd(A.bad, 1);
+            continue;
+        }
+        const size_t to_b = (size_t)to * A.row_bytes, from_b = (size_t)from * A.row_bytes;
+        for (int o = l * 16; o < A.row_bytes; o += 256) {
+            const v4i x = *(const v4i*)((const char*)A.kc + from_b + o);
+            const v4i y = *(const v4i*)((const char*)A.vc + from_b + o);
+            *(v4i*)((char*)A.kc + to_b + o) = x;
+            *(v4i*)((char*)A.vc + to_b + o) = y;
+        }
+        if (A.ks && l == 0) {
+            A.ks[to] = A.ks[from];
+            A.vs[to] = A.vs[from];
+        }
+    }
+}
+
+__global__ void k_kv_take_bad(int32_t* bad, int32_t* out) { *out = atomicExch(bad, 0); }
+
+int check_cache(const dq_kv_ctx* c, const int32_t* table, const void* k, const void* v, const float* ks,
+                const float* vs) {
+    if (!table || !k || !v) DQ_FAIL(DQ_ERR_ARG, "block_table, k_cache and v_cache must not be NULL");
+    if ((c->cache_type == DQ_I8) != (ks != nullptr) || (c->cache_type == DQ_I8) != (vs != nullptr))
+        DQ_FAIL(DQ_ERR_ARG, "an int8 cache has k_scale and v_scale, another has neither");
+    if ((uintptr_t)k % 16 || (uintptr_t)v % 16) DQ_FAIL(DQ_ERR_ARG, "k_cache and v_cache must be 16-byte aligned");
+    if ((uintptr_t)table % 4 || (uintptr_t)ks % 4 || (uintptr_t)vs % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    return dq_kv_check_device(c);
+}
+
+// pairs a lane takes at a time: 4 where the vectors of four pairs are aligned
+// and none straddles the end of the rotated part, else 1
+template <int TI, int TC>
+void launch_append(const AppendArgs& A, int vp, bool il, hipStream_t s) {
+    const dim3 grid((unsigned)((A.groups + 15) / 16)), block(256);
+#define DQ_APPEND(VP_, IL_) hipLaunchKernelGGL((k_kv_append<TI, TC, VP_, IL_>), grid, block, 0, s, A)
+    if (vp == 4) {
+        if constexpr (sizeof(typename Elem<TI>::S) == 2) {
+            if (il) {
+                DQ_APPEND(4, true);
+                return;
+            }
+        }
+        DQ_APPEND(4, false);
+    } else if (il) {
+        DQ_APPEND(1, true);
+    } else {
+        DQ_APPEND(1, false);
+    }
+#undef DQ_APPEND
+}
+
+template <int TI>
+void launch_append_cache(dq_dtype tc, const AppendArgs& A, int vp, bool il, hipStream_t s) {
+    if (tc == DQ_I8) launch_append<TI, DQ_I8>(A, vp, il, s);
+    else if (tc == DQ_BF16) launch_append<TI, DQ_BF16>(A, vp, il, s);
+    else launch_append<TI, DQ_F16>(A, vp, il, s);
+}
+
+template <int TO>
+void launch_read(dq_dtype tc, const ReadArgs& A, hipStream_t s) {
+    const dim3 grid((A.threads + 255) / 256), block(256);
+    if (tc == DQ_I8) hipLaunchKernelGGL((k_kv_read<TO, DQ_I8>), grid, block, 0, s, A);
+    else if (tc == DQ_BF16) hipLaunchKernelGGL((k_kv_read<TO, DQ_BF16>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((k_kv_read<TO, DQ_F16>), grid, block, 0, s, A);
+}
+
+}  // namespace
+
+int dq_kv_check_device(const dq_kv_ctx* c) {
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    if (dev != c->device) DQ_FAIL(DQ_ERR_STATE, "the context belongs to another device");
+    return DQ_OK;
+}
+
+extern "C" int dq_kv_init(dq_kv_ctx** ctx, int batch, int q_heads, int kv_heads, int head_dim, int pages,
+                          int page_size, int pages_per_seq, dq_dtype q_type, dq_dtype cache_type, int gather_scores) {
+    if (!ctx) DQ_FAIL(DQ_ERR_ARG, "ctx is NULL");
+    *ctx = nullptr;
+    if (batch < 1 || q_heads < 1 || kv_heads < 1 || pages < 1 || page_size < 1 || pages_per_seq < 1)
+        DQ_FAIL(DQ_ERR_ARG, "sizes must be >= 1");
+    if (q_heads % kv_heads) DQ_FAIL(DQ_ERR_ARG, "q_heads must be a multiple of kv_heads");
+    if (head_dim < 16 || head_dim % 16) DQ_FAIL(DQ_ERR_ARG, "head_dim must be a positive multiple of 16");
+    if (q_type != DQ_F32 && q_type != DQ_BF16 && q_type != DQ_F16)
+        DQ_FAIL(DQ_ERR_TYPE, "queries must be fp32, bf16 or fp16");
+    if (cache_type != DQ_BF16 && cache_type != DQ_F16 && cache_type != DQ_I8)
+        DQ_FAIL(DQ_ERR_TYPE, "the cache must be bf16, fp16 or int8");
+    if (head_dim > DQ_KV_DIM_MAX) DQ_FAIL(DQ_ERR_RANGE, "head_dim exceeds %d", DQ_KV_DIM_MAX);
+    if (batch > DQ_KV_BATCH_MAX) DQ_FAIL(DQ_ERR_RANGE, "batch exceeds %d", DQ_KV_BATCH_MAX);
+    if ((int64_t)batch * kv_heads > 65535 || (int64_t)batch * q_heads > (1 << 24))
+        DQ_FAIL(DQ_ERR_RANGE, "batch * kv_heads exceeds 65535 or batch * q_heads 2^24");
+    if ((int64_t)pages_per_seq * page_size > (1 << 30))
+        DQ_FAIL(DQ_ERR_RANGE, "pages_per_seq * page_size exceeds 2^30 tokens");
+    if ((__int128)pages * kv_heads * page_size > INT32_MAX)
+        DQ_FAIL(DQ_ERR_RANGE, "pages * kv_heads * page_size exceeds 2^31 - 1 rows");
+    dq_kv_ctx* c = new (std::nothrow) dq_kv_ctx();
+    if (!c) DQ_FAIL(DQ_ERR_ALLOC, "host allocation for the cache context failed");
+    (void)hipGetDevice(&c->device);
+    c->batch = batch;
+    c->Hq = q_heads;
+    c->Hk = kv_heads;
+    c->D = head_dim;
+    c->pages = pages;
+    c->page_size = page_size;
+    c->per_seq = pages_per_seq;
+    c->cap = pages_per_seq * page_size;
+    c->q_type = q_type;
+    c->cache_type = cache_type;
+    c->scores = gather_scores != 0;
+    c->geom.page = make_kvdiv((uint32_t)page_size);
+    c->geom.pages = pages;
+    c->geom.per_seq = pages_per_seq;
+    c->geom.heads = kv_heads;
+    if (hipDeviceGetAttribute(&c->cus, hipDeviceAttributeMultiprocessorCount, c->device) != hipSuccess || c->cus < 1)
+        c->cus = 256;
+    // a head's moves: at most half its slots come free and as many fill them
+    c->moves_stride = (size_t)c->cap / 2 + 1;
+    const size_t moves = (size_t)batch * kv_heads * (1 + 2 * c->moves_stride);
+    c->part_floats = dq_attend_part_floats(c);
+    if (c->scores) c->s_stride = ((size_t)c->cap + 127) / 128 * 128;
+    bool ok = hipMalloc(&c->bad, 8) == hipSuccess && hipMalloc(&c->moves, moves * 4) == hipSuccess &&
+              (!c->part_floats || hipMalloc(&c->part, c->part_floats * 4) == hipSuccess) &&
+              (!c->scores || hipMalloc(&c->s, (size_t)batch * q_heads * c->s_stride * 4) == hipSuccess);
+    if (!ok) {
+        dq_kv_release(c);
+        DQ_FAIL(DQ_ERR_ALLOC, "device allocation for the cache context failed");
+    }
+    if (hipMemset(c->bad, 0, 8) != hipSuccess) {
+        dq_kv_release(c);
+        DQ_FAIL(DQ_ERR_HIP, "clearing the cache context failed");
+    }
+    const char* names[] = {"fp32", "bf16", "int8", "uint8", "fp16"};
+    snprintf(c->info, sizeof c->info, "gfx950 paged cache: %d sequences, %d query and %d key-value heads of %d, %d pages "
+             "of %d, %s queries, %s cache", batch, q_heads, kv_heads, head_dim, pages, page_size, names[q_type],
+             names[cache_type]);
+    *ctx = c;
+    return DQ_OK;
+}
+
+extern "C" int dq_kv_append(dq_kv_ctx* ctx, int64_t tokens, const void* k, int64_t k_token_stride,
+                            int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                            const int32_t* index, const int32_t* seq_ids, const int32_t* block_table, void* k_cache,
+                            void* v_cache, float* k_scale, float* v_scale, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, void* q_out, const dq_rope_ctx* rope, const int32_t* positions,
+                            void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (tokens < 0) DQ_FAIL(DQ_ERR_ARG, "tokens must be >= 0");
+    if (tokens == 0) return DQ_OK;
+    if (!k || !v || !index) DQ_FAIL(DQ_ERR_ARG, "k, v and index must not be NULL");
+    if ((q != nullptr) != (q_out != nullptr)) DQ_FAIL(DQ_ERR_ARG, "q and q_out go together");
+    if ((rope != nullptr) != (positions != nullptr)) DQ_FAIL(DQ_ERR_ARG, "rope and positions go together");
+    if (!seq_ids && tokens > ctx->batch) DQ_FAIL(DQ_ERR_ARG, "more tokens than sequences need seq_ids");
+    if (rope && rope->D != ctx->D) DQ_FAIL(DQ_ERR_ARG, "the rotary context's head_dim is not the cache's");
+    const size_t es = kv_elem_bytes(ctx->q_type);
+    if ((uintptr_t)k % es || (uintptr_t)v % es || (uintptr_t)q % es || (uintptr_t)q_out % es ||
+        (uintptr_t)index % 4 || (uintptr_t)seq_ids % 4 || (uintptr_t)positions % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if (q && q == q_out && (q_head_stride != ctx->D || q_token_stride != (int64_t)ctx->Hq * ctx->D))
+        DQ_FAIL(DQ_ERR_ARG, "q_out is dense: in place q has to be dense too");
+    if (int rc = check_cache(ctx, block_table, k_cache, v_cache, k_scale, v_scale)) return rc;
+    if (rope)
+        if (int rc = dq_rope_check_device(rope)) return rc;
+    if (tokens > INT32_MAX / 16) DQ_FAIL(DQ_ERR_RANGE, "too many tokens for one launch");
+    AppendArgs A{};
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.q_out = q_out;
+    A.qt = q_token_stride;
+    A.qh = q_head_stride;
+    A.kt = k_token_stride;
+    A.kh = k_head_stride;
+    A.vt = v_token_stride;
+    A.vh = v_head_stride;
+    A.index = index;
+    A.seq_ids = seq_ids;
+    A.table = block_table;
+    A.kc = k_cache;
+    A.vc = v_cache;
+    A.ks = k_scale;
+    A.vs = v_scale;
+    A.bad = ctx->bad;
+    A.pos = positions;
+    A.freq = rope ? rope->freq : nullptr;
+    A.axis = rope ? rope->axis : nullptr;
+    A.tokens = (int)tokens;
+    A.batch = ctx->batch;
+    A.Hq = q ? ctx->Hq : 0;
+    A.Hk = ctx->Hk;
+    A.D = ctx->D;
+    A.R = rope ? rope->R : ctx->D;
+    A.geom = ctx->geom;
+    // rows per group: as many as leave the chip filled (2^14 groups), at most 8
+    const int64_t rows = A.Hq + 2 * (int64_t)A.Hk;
+    int chunk = 1;
+    while (chunk < 8 && tokens * (rows / (2 * chunk)) >= (1 << 14)) chunk *= 2;
+    A.chunk = chunk;
+    const int64_t chunks = (rows + chunk - 1) / chunk;
+    A.chunks = make_kvdiv((uint32_t)chunks);
+    A.groups = tokens * chunks;
+    if (A.groups > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many tokens for one launch");
+    const bool il = rope && rope->interleaved;
+    const size_t bytes = (il ? 8 : 4) * es;
+    bool wide = A.R / 2 % 4 == 0 && bytes <= 16 && (uintptr_t)k % bytes == 0 && (uintptr_t)v % bytes == 0 &&
+                (uintptr_t)q % bytes == 0 && (uintptr_t)q_out % bytes == 0;
+    const long long st[6] = {A.qt, A.qh, A.kt, A.kh, A.vt, A.vh};
+    for (int i = q ? 0 : 2; i < 6; ++i) wide = wide && st[i] % (il ? 8 : 4) == 0;
+    const hipStream_t s = (hipStream_t)stream;
+    const int vp = wide ? 4 : 1;
+    if (ctx->q_type == DQ_F32) launch_append_cache<DQ_F32>(ctx->cache_type, A, vp, il, s);
+    else if (ctx->q_type == DQ_BF16) launch_append_cache<DQ_BF16>(ctx->cache_type, A, vp, il, s);
+    else launch_append_cache<DQ_F16>(ctx->cache_type, A, vp, il, s);
+    DQ_LAUNCH_CHECK("cache append");
+    return DQ_OK;
+}
+
+extern "C" int dq_kv_read(dq_kv_ctx* ctx, int64_t tokens, const int32_t* index, const int32_t* seq_ids,
+                          const int32_t* block_table, const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, void* k_out, void* v_out, void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (tokens < 0) DQ_FAIL(DQ_ERR_ARG, "tokens must be >= 0");
+    if (tokens == 0) return DQ_OK;
+    if (!index || (!k_out && !v_out)) DQ_FAIL(DQ_ERR_ARG, "index and one of k_out and v_out must not be NULL");
+    if (!seq_ids && tokens > ctx->batch) DQ_FAIL(DQ_ERR_ARG, "more tokens than sequences need seq_ids");
+    if ((uintptr_t)k_out % 16 || (uintptr_t)v_out % 16) DQ_FAIL(DQ_ERR_ARG, "k_out and v_out must be 16-byte aligned");
+    if ((uintptr_t)index % 4 || (uintptr_t)seq_ids % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if (int rc = check_cache(ctx, block_table, k_cache, v_cache, k_scale, v_scale)) return rc;
+    const int64_t pieces = ctx->D / 8;
+    if (tokens > INT32_MAX || tokens * ctx->Hk > INT32_MAX || tokens * ctx->Hk * pieces > (int64_t)UINT32_MAX - 256)
+        DQ_FAIL(DQ_ERR_RANGE, "too many tokens for one launch");
+    ReadArgs A{};
+    A.index = index;
+    A.seq_ids = seq_ids;
+    A.table = block_table;
+    A.kc = k_cache;
+    A.vc = v_cache;
+    A.ks = k_scale;
+    A.vs = v_scale;
+    A.k_out = k_out;
+    A.v_out = v_out;
+    A.bad = ctx->bad;
+    A.threads = (uint32_t)(tokens * ctx->Hk * pieces);
+    A.Hk = ctx->Hk;
+    A.D = ctx->D;
+    A.batch = ctx->batch;
+    A.pieces = make_kvdiv((uint32_t)pieces);
+    A.heads = make_kvdiv((uint32_t)ctx->Hk);
+    A.geom = ctx->geom;
+    const hipStream_t s = (hipStream_t)stream;
+    if (ctx->q_type == DQ_F32) launch_read<DQ_F32>(ctx->cache_type, A, s);
+    else if (ctx->q_type == DQ_BF16) launch_read<DQ_BF16>(ctx->cache_type, A, s);
+    else launch_read<DQ_F16>(ctx->cache_type, A, s);
+    DQ_LAUNCH_CHECK("cache read");
+    return DQ_OK;
+}
+
+extern "C" int dq_kv_attend(dq_kv_ctx* ctx, int batch, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t* lens, const int32_t* block_table, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, void* out, float sm_scale, float* lse,
+                            int window, const float* scores, float* scores_out, float decay, void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (batch < 0 || batch > ctx->batch) DQ_FAIL(DQ_ERR_ARG, "batch must lie in [0, %d]", ctx->batch);
+    if (batch == 0) return DQ_OK;
+    if (!q || !lens || !out) DQ_FAIL(DQ_ERR_ARG, "q, lens and out must not be NULL");
+    if (window < 0) DQ_FAIL(DQ_ERR_ARG, "window must be >= 0 (0: none)");
+    if (!isfinite(sm_scale)) DQ_FAIL(DQ_ERR_ARG, "sm_scale must be finite");
+    if ((scores != nullptr) != (scores_out != nullptr)) DQ_FAIL(DQ_ERR_ARG, "scores and scores_out go together");
+    if (scores && !ctx->scores) DQ_FAIL(DQ_ERR_STATE, "the context was made without gather_scores");
+    const size_t es = kv_elem_bytes(ctx->q_type);
+    if ((uintptr_t)q % es || (uintptr_t)lens % 4 || (uintptr_t)lse % 4 || (uintptr_t)scores % 4 ||
+        (uintptr_t)scores_out % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if ((uintptr_t)out % 16) DQ_FAIL(DQ_ERR_ARG, "out must be 16-byte aligned");
+    if (int rc = check_cache(ctx, block_table, k_cache, v_cache, k_scale, v_scale)) return rc;
+    const DqAttendArgs A{q,   q_token_stride, q_head_stride, lens,   block_table, k_cache,    v_cache, k_scale, v_scale,
+                         out, lse,            batch,         sm_scale, window,    scores, scores_out, decay};
+    return dq_launch_attend(ctx, A, (hipStream_t)stream);
+}
+
+extern "C" int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, int sinks, const int32_t* lens,
+                           const int32_t* newest, const float* scores, const int32_t* order,
+                           const int32_t* block_table, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                           float* scores_out, int32_t* order_out, int32_t* lens_out, void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (batch < 0 || batch > ctx->batch) DQ_FAIL(DQ_ERR_ARG, "batch must lie in [0, %d]", ctx->batch);
+    if (budget < 1 || recent < 0 || sinks < 0) DQ_FAIL(DQ_ERR_ARG, "budget must be >= 1, recent and sinks >= 0");
+    if (batch == 0) return DQ_OK;
+    if (!lens || !newest || !scores || !order || !scores_out || !order_out || !lens_out)
+        DQ_FAIL(DQ_ERR_ARG, "lens, newest, scores, order and their outputs must not be NULL");
+    if ((uintptr_t)lens % 4 || (uintptr_t)newest % 4 || (uintptr_t)scores % 4 || (uintptr_t)order % 4 ||
+        (uintptr_t)scores_out % 4 || (uintptr_t)order_out % 4 || (uintptr_t)lens_out % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if (int rc = check_cache(ctx, block_table, k_cache, v_cache, k_scale, v_scale)) return rc;
+    EvictArgs A{};
+    A.lens = lens;
+    A.newest = newest;
+    A.scores = scores;
+    A.order = order;
+    A.table = block_table;
+    A.kc = k_cache;
+    A.vc = v_cache;
+    A.ks = k_scale;
+    A.vs = v_scale;
+    A.scores_out = scores_out;
+    A.order_out = order_out;
+    A.lens_out = lens_out;
+    A.moves = ctx->moves;
+    A.moves_stride = ctx->moves_stride;
+    A.bad = ctx->bad;
+    A.batch = batch;
+    A.Hk = ctx->Hk;
+    A.cap = ctx->cap;
+    A.budget = budget;
+    A.sinks = sinks;
+    A.recent = recent;
+    A.row_bytes = ctx->D * (int)kv_elem_bytes(ctx->cache_type);
+    A.geom = ctx->geom;
+    const hipStream_t s = (hipStream_t)stream;
+    const int items = batch * ctx->Hk;
+    hipLaunchKernelGGL(k_kv_evict_select, dim3((unsigned)items), dim3(kSelThreads), 0, s, A);
+    DQ_LAUNCH_CHECK("eviction's selection");
+    // workgroups for the most rows that can move, at most 2^14 in all
+    const int most = std::max(1, std::min(budget, ctx->cap - budget));
+    const int gx = std::max(1, std::min((most + 15) / 16, (1 << 14) / items));
+    hipLaunchKernelGGL(k_kv_evict_move, dim3((unsigned)gx, (unsigned)items), dim3(256), 0, s, A);
+    DQ_LAUNCH_CHECK("eviction's moves");
+    return DQ_OK;
+}
+
+extern "C" int dq_kv_take_errors(dq_kv_ctx* ctx, int* count, void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (!count) DQ_FAIL(DQ_ERR_ARG, "count must not be NULL");
+    if (int rc = dq_kv_check_device(ctx)) return rc;
+    const hipStream_t s = (hipStream_t)stream;
+    hipLaunchKernelGGL(k_kv_take_bad, dim3(1), dim3(1), 0, s, ctx->bad, ctx->bad + 1);
+    DQ_LAUNCH_CHECK("cache error count");
+    DQ_HIP_CHECK(hipMemcpyAsync(count, ctx->bad + 1, 4, hipMemcpyDeviceToHost, s));
+    DQ_HIP_CHECK(hipStreamSynchronize(s));
+    return DQ_OK;
+}
+
+extern "C" const char* dq_kv_info(const dq_kv_ctx* ctx) { return ctx ? ctx->info : nullptr; }
+
+extern "C" void dq_kv_release(dq_kv_ctx* ctx) {
+    if (!ctx) return;
+    (void)hipFree(ctx->bad);
+    (void)hipFree(ctx->moves);
+    (void)hipFree(ctx->part);
+    (void)hipFree(ctx->s);
+    delete ctx;
+}

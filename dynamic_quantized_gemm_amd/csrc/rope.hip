@@ -1,0 +1,256 @@
+// rope.hip -- rotary positions with several axes.
+//
+// Pair i of a token's head turns by the angle pos[axis(i)] * inv_freq[i]:
+//   (a, b) -> (a cos - b sin, b cos + a sin),
+// and by the opposite angle for the inverse, which is also the gradient's
+// pass (the rotation is orthogonal). Elements past the rotated part pass
+// through unchanged.
+//
+// Bound by the traffic of x and y. A thread keeps the cosines and sines of VP
+// pairs in registers and walks heads with them, so an angle is computed once
+// for each thread's run of heads and x is read and y written once, VP
+// elements (up to 16 bytes) at a time.
+#include <math.h>
+#include <stdio.h>
+
+#include <algorithm>
+#include <new>
+
+#include "paged_kv.h"
+
+using namespace dq;
+
+namespace {
+
+struct RopeArgs {
+    const void* x;
+    void* y;
+    const int32_t* pos;
+    const double2* freq;
+    const int32_t* axis;
+    long long xt, xh, yt, yh;
+    uint32_t threads;  // tokens * chunks * lanes
+    int tokens, heads, D, R, inverse;
+    int chunk;         // heads a thread walks
+    KvDiv lanes, chunks;
+};
+
+template <int TYPE, int VP, bool IL>
+__global__ void __launch_bounds__(256) k_rope(const RopeArgs A) {
+    typedef typename Elem<TYPE>::S S;
+    const uint32_t id = blockIdx.x * 256u + threadIdx.x;
+    if (id >= A.threads) return;
+    const uint32_t rest = kv_div(id, A.lanes);
+    const int i0 = (int)(id - rest * A.lanes.d) * VP;
+    const uint32_t t = kv_div(rest, A.chunks);
+    const int h0 = (int)(rest - t * A.chunks.d) * A.chunk;
+    const int h1 = min(A.heads, h0 + A.chunk);
+    const bool turn = i0 < A.R / 2;
+    float c[VP], s[VP];
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+        c[i] = 1.0f;
+        s[i] = 0.0f;
+        if (turn) rope_cos_sin(A.pos[(size_t)A.axis[i0 + i] * A.tokens + t], A.freq[i0 + i], &c[i], &s[i]);
+        if (A.inverse) s[i] = -s[i];
+    }
+    int lo, hi;
+    kv_pair(i0, A.D, A.R, IL, &lo, &hi);
+    const S* x = (const S*)A.x + t * A.xt;
+    S* y = (S*)A.y + t * A.yt;
+#pragma unroll 4
+    for (int h = h0; h < h1; ++h) {
+        const S* xr = x + h * A.xh;
+        S* yr = y + h * A.yh;
+        float a[VP], b[VP];
+        if (IL) {
+            float e[2 * VP];
+            load_vec(xr + lo, e);
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                a[i] = e[2 * i];
+                b[i] = e[2 * i + 1];
+            }
+        } else {
+            load_vec(xr + lo, a);
+            load_vec(xr + hi, b);
+        }
+        if (turn) {
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                const float u = a[i] * c[i] - b[i] * s[i];
+                b[i] = b[i] * c[i] + a[i] * s[i];
+                a[i] = u;
+            }
+        }
+        if (IL) {
+            float e[2 * VP];
+#pragma unroll
+            for (int i = 0; i < VP; ++i) {
+                e[2 * i] = a[i];
+                e[2 * i + 1] = b[i];
+            }
+            store_vec(yr + lo, e);
+        } else {
+            store_vec(yr + lo, a);
+            store_vec(yr + hi, b);
+        }
+    }
+}
+
+// the largest number of pairs a thread can take: the vectors of VP (or, for
+// neighbouring pairs, 2 VP) elements have to be aligned in x and y and must
+// not straddle the end of the rotated part
+int pick_vp(const dq_rope_ctx* c, size_t es, const void* x, const void* y, const long long* strides) {
+    for (int vp = 16 / (int)es; vp > 1; vp /= 2) {
+        const int elems = c->interleaved ? 2 * vp : vp;
+        const size_t bytes = elems * es;
+        if (bytes > 16) continue;
+        bool ok = (c->R / 2) % vp == 0 && (c->D - c->R) / 2 % vp == 0;
+        if (c->interleaved) ok = ok && c->R % (2 * vp) == 0 && c->D % (2 * vp) == 0;
+        ok = ok && (uintptr_t)x % bytes == 0 && (uintptr_t)y % bytes == 0;
+        for (int i = 0; i < 4; ++i) ok = ok && strides[i] % elems == 0;
+        if (ok) return vp;
+    }
+    return 1;
+}
+
+template <int TYPE, int VP>
+void launch(const RopeArgs& A, bool il, hipStream_t s) {
+    const dim3 grid((A.threads + 255) / 256), block(256);
+    if constexpr (2 * VP * sizeof(typename Elem<TYPE>::S) <= 16) {
+        if (il) {
+            hipLaunchKernelGGL((k_rope<TYPE, VP, true>), grid, block, 0, s, A);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_rope<TYPE, VP, false>), grid, block, 0, s, A);
+}
+
+template <int TYPE>
+void launch_type(const RopeArgs& A, int vp, bool il, hipStream_t s) {
+    switch (vp) {
+        case 8:
+            if constexpr (TYPE != DQ_F32) launch<TYPE, 8>(A, il, s);
+            break;
+        case 4: launch<TYPE, 4>(A, il, s); break;
+        case 2: launch<TYPE, 2>(A, il, s); break;
+        default: launch<TYPE, 1>(A, il, s); break;
+    }
+}
+
+}  // namespace
+
+int dq_rope_check_device(const dq_rope_ctx* c) {
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    if (dev != c->device) DQ_FAIL(DQ_ERR_STATE, "the context belongs to another device");
+    return DQ_OK;
+}
+
+extern "C" int dq_rope_init(dq_rope_ctx** ctx, int head_dim, int rotary_dim, const int32_t* axis_of_pair,
+                            const double* inv_freq, int interleaved) {
+    if (!ctx) DQ_FAIL(DQ_ERR_ARG, "ctx is NULL");
+    *ctx = nullptr;
+    if (head_dim < 2 || head_dim % 2 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim)
+        DQ_FAIL(DQ_ERR_ARG, "head_dim and rotary_dim must be even, 2 <= rotary_dim <= head_dim");
+    if (head_dim > DQ_ROPE_DIM_MAX) DQ_FAIL(DQ_ERR_RANGE, "head_dim exceeds %d", DQ_ROPE_DIM_MAX);
+    if (!axis_of_pair || !inv_freq) DQ_FAIL(DQ_ERR_ARG, "axis_of_pair and inv_freq must not be NULL");
+    const int P = rotary_dim / 2;
+    int axes = 1;
+    for (int i = 0; i < P; ++i) {
+        if (axis_of_pair[i] < 0 || axis_of_pair[i] >= DQ_ROPE_AXES_MAX)
+            DQ_FAIL(DQ_ERR_RANGE, "axis %d of pair %d is outside [0, %d)", axis_of_pair[i], i, DQ_ROPE_AXES_MAX);
+        if (!isfinite(inv_freq[i]) || fabs(inv_freq[i]) > 1e9)
+            DQ_FAIL(DQ_ERR_ARG, "inv_freq of pair %d is not finite or beyond 1e9", i);
+        axes = std::max(axes, axis_of_pair[i] + 1);
+    }
+    double2 freq[DQ_ROPE_DIM_MAX / 2];
+    for (int i = 0; i < P; ++i) {
+        const long double turns = (long double)inv_freq[i] / 6.283185307179586476925286766559L;
+        freq[i].x = (double)turns;
+        freq[i].y = (double)(turns - (long double)freq[i].x);
+    }
+    dq_rope_ctx* c = new (std::nothrow) dq_rope_ctx();
+    if (!c) DQ_FAIL(DQ_ERR_ALLOC, "host allocation for the rotary context failed");
+    (void)hipGetDevice(&c->device);
+    c->D = head_dim;
+    c->R = rotary_dim;
+    c->axes = axes;
+    c->interleaved = interleaved ? 1 : 0;
+    if (hipMalloc(&c->freq, P * sizeof(double2)) != hipSuccess || hipMalloc(&c->axis, P * 4) != hipSuccess) {
+        dq_rope_release(c);
+        DQ_FAIL(DQ_ERR_ALLOC, "device allocation for the rotary context failed");
+    }
+    if (hipMemcpy(c->freq, freq, P * sizeof(double2), hipMemcpyHostToDevice) != hipSuccess ||
+        hipMemcpy(c->axis, axis_of_pair, P * 4, hipMemcpyHostToDevice) != hipSuccess) {
+        dq_rope_release(c);
+        DQ_FAIL(DQ_ERR_HIP, "copy of the rotary frequencies failed");
+    }
+    snprintf(c->info, sizeof c->info, "gfx950 rotary positions: %d of %d elements, %d axes, pairs of %s", rotary_dim, head_dim,
+             axes, interleaved ? "neighbours" : "halves");
+    *ctx = c;
+    return DQ_OK;
+}
+
+extern "C" int dq_rope_forward(const dq_rope_ctx* ctx, const void* x, dq_dtype type, int64_t tokens, int heads,
+                               int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions, void* y,
+                               int64_t y_token_stride, int64_t y_head_stride, int inverse, void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (type != DQ_F32 && type != DQ_BF16 && type != DQ_F16) DQ_FAIL(DQ_ERR_TYPE, "x must be fp32, bf16 or fp16");
+    if (tokens < 0 || heads < 0) DQ_FAIL(DQ_ERR_ARG, "negative sizes");
+    if (tokens == 0 || heads == 0) return DQ_OK;
+    if (!x || !y || !positions) DQ_FAIL(DQ_ERR_ARG, "x, y and positions must not be NULL");
+    const size_t es = kv_elem_bytes(type);
+    if ((uintptr_t)x % es || (uintptr_t)y % es || (uintptr_t)positions % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if (x == y && (x_token_stride != y_token_stride || x_head_stride != y_head_stride))
+        DQ_FAIL(DQ_ERR_ARG, "in place the strides of x and y must be the same");
+    if (tokens > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many tokens for one launch");
+    if (int rc = dq_rope_check_device(ctx)) return rc;
+    RopeArgs A{};
+    A.x = x;
+    A.y = y;
+    A.pos = positions;
+    A.freq = ctx->freq;
+    A.axis = ctx->axis;
+    A.xt = x_token_stride;
+    A.xh = x_head_stride;
+    A.yt = y_token_stride;
+    A.yh = y_head_stride;
+    A.heads = heads;
+    A.D = ctx->D;
+    A.R = ctx->R;
+    A.inverse = inverse ? 1 : 0;
+    const long long st[4] = {A.xt, A.xh, A.yt, A.yh};
+    const int vp = pick_vp(ctx, es, x, y, st);
+    const int64_t lanes = ctx->D / 2 / vp;
+    // heads per thread: as many as leave the chip filled (2^18 threads), at most 8
+    int chunk = 1;
+    while (chunk < 8 && chunk < heads && tokens * ((heads - 1) / (2 * chunk) + 1) * lanes >= (1 << 18))
+        chunk *= 2;
+    const int64_t chunks = (heads - 1) / chunk + 1;
+    if (tokens * chunks > INT32_MAX || tokens * chunks * lanes > (int64_t)UINT32_MAX - 256)
+        DQ_FAIL(DQ_ERR_RANGE, "too many tokens for one launch");
+    A.tokens = (int)tokens;
+    A.chunk = chunk;
+    A.lanes = make_kvdiv((uint32_t)lanes);
+    A.chunks = make_kvdiv((uint32_t)chunks);
+    A.threads = (uint32_t)(tokens * chunks * lanes);
+    const hipStream_t s = (hipStream_t)stream;
+    const bool il = ctx->interleaved;
+    if (type == DQ_F32) launch_type<DQ_F32>(A, vp, il, s);
+    else if (type == DQ_BF16) launch_type<DQ_BF16>(A, vp, il, s);
+    else launch_type<DQ_F16>(A, vp, il, s);
+    DQ_LAUNCH_CHECK("rotary positions");
+    return DQ_OK;
+}
+
+extern "C" const char* dq_rope_info(const dq_rope_ctx* ctx) { return ctx ? ctx->info : nullptr; }
+
+extern "C" void dq_rope_release(dq_rope_ctx* ctx) {
+    if (!ctx) return;
+    (void)hipFree(ctx->freq);
+    (void)hipFree(ctx->axis);
+    delete ctx;
+}

@@ -1,6 +1,7 @@
 /*
- * dqip.h -- C ABI of libdqip.so: the dynamic quantized inner product and the
- * QuantizeLinear / DequantizeLinear element-wise operators on one AMD
+ * dqip.h -- C ABI of libdqip.so: the dynamic quantized inner product, the
+ * QuantizeLinear / DequantizeLinear element-wise operators, the quantized
+ * operators around them and decoding over a paged key-value cache on one AMD
  * Instinct MI355X (gfx950).
  *
  * Conventions for every entry point
@@ -626,6 +627,160 @@ int dq_lstm_forward(dq_lstm_ctx* ctx, const float* X, const int32_t* sequence_le
 const char* dq_lstm_info(const dq_lstm_ctx* ctx);
 /* Frees the context and its device memory; NULL is a no-op. */
 void dq_lstm_release(dq_lstm_ctx* ctx);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions with several axes.
+ * Pair i < rotary_dim / 2 of a head turns by pos[axis(i)] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * where the pair is elements (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved != 0; elements from rotary_dim on pass through. inverse != 0
+ * turns by the opposite angle: the rotation is orthogonal, so that is also
+ * the gradient's pass (the gradient of x from that of y). The angle is the
+ * exact product reduced to one turn in fp64, cos and sin are rounded to fp32
+ * once; the rotation is fp32 (two products, then their sum) and rounded to
+ * x's type once.
+ *
+ * dq_rope_init: head_dim, rotary_dim even, 2 <= rotary_dim <= head_dim <=
+ * DQ_ROPE_DIM_MAX; axis_of_pair (HOST, rotary_dim / 2 values in [0,
+ * DQ_ROPE_AXES_MAX)); inv_freq (HOST, rotary_dim / 2 values, finite, magnitude
+ * at most 1e9). Copies both to the device (synchronizes). Errors: DQ_ERR_ARG,
+ * DQ_ERR_RANGE, DQ_ERR_ALLOC, DQ_ERR_HIP.
+ * dq_rope_forward: x and y (DEVICE, DQ_F32 / DQ_BF16 / DQ_F16) hold `tokens`
+ * tokens of `heads` heads; element (t, h, d) lies at t * token_stride + h *
+ * head_stride + d (strides in elements: a slice of a fused projection is
+ * read where it lies). positions: int32 [axes, tokens] (DEVICE, dense), axes
+ * = 1 + the largest axis. y may be x with the same strides; otherwise they
+ * must not overlap. Asynchronous on `stream`, needs no workspace: calls may
+ * overlap. Zero tokens or heads is a no-op. Errors: DQ_ERR_STATE,
+ * DQ_ERR_TYPE, DQ_ERR_ARG, DQ_ERR_RANGE (beyond one launch), DQ_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+#define DQ_ROPE_DIM_MAX 1024
+#define DQ_ROPE_AXES_MAX 8
+
+typedef struct dq_rope_ctx dq_rope_ctx;
+
+int dq_rope_init(dq_rope_ctx** ctx, int head_dim, int rotary_dim, const int32_t* axis_of_pair,
+                 const double* inv_freq, int interleaved);
+int dq_rope_forward(const dq_rope_ctx* ctx, const void* x, dq_dtype type, int64_t tokens, int heads,
+                    int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions, void* y,
+                    int64_t y_token_stride, int64_t y_head_stride, int inverse, void* stream);
+/* A short description of the context (owned by it); NULL for NULL. */
+const char* dq_rope_info(const dq_rope_ctx* ctx);
+/* Frees the context and its device memory; NULL is a no-op. */
+void dq_rope_release(dq_rope_ctx* ctx);
+
+/* ------------------------------------------------------------------------
+ * Decoding over a paged key-value cache.
+ * The cache: k_cache and v_cache [pages, kv_heads, page_size, head_dim]
+ * (DEVICE, dense, 16-byte aligned) of bf16, fp16 or int8; an int8 cache has
+ * one fp32 scale for every row of head_dim codes, k_scale and v_scale
+ * [pages, kv_heads, page_size] (another cache: both NULL). block_table: int32
+ * [batch, pages_per_seq] (DEVICE, dense); slot t of sequence b lies in page
+ * block_table[b, t / page_size] at t % page_size. Entries past those that a
+ * call needs are not read. Query head h belongs to key-value head
+ * h / (q_heads / kv_heads). cap = pages_per_seq * page_size.
+ *
+ * What cannot be checked on the host is checked in the kernels: a block
+ * table entry outside [0, pages), a sequence number outside [0, batch), an
+ * index of cap or more and a length outside [0, cap] are never followed to
+ * memory; each call says below what it gives then, and dq_kv_take_errors
+ * counts them.
+ *
+ * dq_kv_init: batch, heads and pages >= 1, q_heads a multiple of kv_heads,
+ * head_dim a multiple of 16 up to DQ_KV_DIM_MAX, batch <= DQ_KV_BATCH_MAX,
+ * cap <= 2^30, pages * kv_heads * page_size < 2^31; q_type (DQ_F32 / DQ_BF16 /
+ * DQ_F16) of queries, new keys and values, and outputs; cache_type (DQ_BF16 /
+ * DQ_F16 / DQ_I8), each with each. gather_scores != 0 lets dq_kv_attend gather
+ * weights (batch * q_heads * cap fp32 more of workspace). Allocates every
+ * device buffer of the context (none later). Errors: DQ_ERR_ARG, DQ_ERR_TYPE,
+ * DQ_ERR_RANGE, DQ_ERR_ALLOC, DQ_ERR_HIP.
+ *
+ * All calls are asynchronous on `stream` and allocate nothing. dq_kv_attend
+ * and dq_kv_evict use the context's workspace: their calls on one context must
+ * not overlap. Common errors: DQ_ERR_STATE (no context, another device),
+ * DQ_ERR_ARG (NULL or misaligned tensor, sizes), DQ_ERR_RANGE (beyond one
+ * launch), DQ_ERR_HIP.
+ *
+ * dq_kv_append: stores `tokens` new keys and values, k and v (element (t, h,
+ * d) at t * token_stride + h * head_stride + d), at slot index[t] (int32) of
+ * sequence seq_ids[t] (int32; NULL: of sequence t, at most batch tokens). With
+ * rope and positions (both or neither) keys are rotated as dq_rope_forward
+ * does, before anything is rounded. q and q_out (both or neither): the
+ * queries rotated too, into a dense [tokens, q_heads, head_dim] (q_out = q is
+ * allowed where q is dense). int8: scale = max|row| / 127 (1 where that is not
+ * > 0), code = sat[-127,127](rne(row / scale)), IEEE fp32; a row that is not
+ * finite is stored as zeros with a NaN scale. index < 0: nothing is stored
+ * (q_out is still written). Two tokens of one call for one slot: either is
+ * stored, or a mix. A place that does not exist: nothing is stored, counted.
+ *
+ * dq_kv_read: rows back as values of q_type, k_out and v_out [tokens,
+ * kv_heads, head_dim] (16-byte aligned, either may be NULL): the stored value,
+ * or code * scale, rounded once. index < 0 gives zeros, a place that does not
+ * exist NaN.
+ *
+ * dq_kv_attend: q (strided as k above) [batch, q_heads, head_dim], lens int32
+ * [batch] (DEVICE), batch <= the context's, to out [batch, q_heads, head_dim]
+ * (dense, 16-byte aligned). Sequence b attends to its tokens t in
+ * [max(0, len - window), len) (window 0: from 0):
+ *   s_t = sm_scale q . k_t,  p = softmax(s),  out = sum_t p_t v_t,
+ *   lse = log sum_t exp(s_t)     ([batch, q_heads] fp32, may be NULL)
+ * No token (or only weights of zero): out 0, lse -infinity. Sums and softmax
+ * are fp32; a NaN or infinity in a row outside the range has no effect.
+ * scores and scores_out ([batch, kv_heads, cap] fp32, both or neither, may be
+ * the same): for t < len
+ *   scores_out = decay * scores + the sum of p_t over the query heads of the
+ * key-value head (p_t = 0 before the window); other entries are left alone.
+ * A page that does not exist, or a length out of range: out and lse of the
+ * sequence's heads that need it are NaN.
+ *
+ * dq_kv_evict: every head of a sequence with len > budget is cut down to
+ * `budget` tokens. Of its slots [0, len) those with order < sinks or order >
+ * newest[b] - recent stay first (order: the token's running number, int32
+ * [batch, kv_heads, cap]; newest int32 [batch]), then those of the largest
+ * scores ([batch, kv_heads, cap] fp32, a NaN above everything; ties, and more
+ * such tokens than fit, go to the lowest slot). Kept tokens at slots from
+ * budget on move, in order, into the slots below it that came free: rows and
+ * scales in the cache, scores and order into scores_out and order_out, whose
+ * entries from the new length on are left alone. lens_out = min(len, budget).
+ * scores_out, order_out and lens_out may be their inputs. The budget is >= 1.
+ * A move from or to a page that does not exist leaves the cache's row alone.
+ *
+ * dq_kv_take_errors: how many such places the calls before it met (as their
+ * kernels counted them: one place can count more than once), and clears the
+ * count. Synchronizes `stream`.
+ * ---------------------------------------------------------------------- */
+#define DQ_KV_DIM_MAX 256
+#define DQ_KV_BATCH_MAX 65535
+
+typedef struct dq_kv_ctx dq_kv_ctx;
+
+int dq_kv_init(dq_kv_ctx** ctx, int batch, int q_heads, int kv_heads, int head_dim, int pages,
+               int page_size, int pages_per_seq, dq_dtype q_type, dq_dtype cache_type,
+               int gather_scores);
+int dq_kv_append(dq_kv_ctx* ctx, int64_t tokens, const void* k, int64_t k_token_stride,
+                 int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                 int64_t v_head_stride, const int32_t* index, const int32_t* seq_ids,
+                 const int32_t* block_table, void* k_cache, void* v_cache, float* k_scale,
+                 float* v_scale, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                 void* q_out, const dq_rope_ctx* rope, const int32_t* positions, void* stream);
+int dq_kv_read(dq_kv_ctx* ctx, int64_t tokens, const int32_t* index, const int32_t* seq_ids,
+               const int32_t* block_table, const void* k_cache, const void* v_cache,
+               const float* k_scale, const float* v_scale, void* k_out, void* v_out, void* stream);
+int dq_kv_attend(dq_kv_ctx* ctx, int batch, const void* q, int64_t q_token_stride,
+                 int64_t q_head_stride, const int32_t* lens, const int32_t* block_table,
+                 const void* k_cache, const void* v_cache, const float* k_scale,
+                 const float* v_scale, void* out, float sm_scale, float* lse, int window,
+                 const float* scores, float* scores_out, float decay, void* stream);
+int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, int sinks, const int32_t* lens,
+                const int32_t* newest, const float* scores, const int32_t* order,
+                const int32_t* block_table, void* k_cache, void* v_cache, float* k_scale,
+                float* v_scale, float* scores_out, int32_t* order_out, int32_t* lens_out,
+                void* stream);
+int dq_kv_take_errors(dq_kv_ctx* ctx, int* count, void* stream);
+/* A short description of the context (owned by it); NULL for NULL. */
+const char* dq_kv_info(const dq_kv_ctx* ctx);
+/* Frees the context and its device memory; NULL is a no-op. */
+void dq_kv_release(dq_kv_ctx* ctx);
 
 #ifdef __cplusplus
 }
