@@ -1,0 +1,514 @@
+// attend_kernel.h -- the attention kernel over the paged cache, a template on
+// the cache's type; paged_attend_*.hip hold its instances.
+//
+//   s_t = sm_scale q . k_t     for the tokens t in [max(0, len - window), len)
+//   p   = softmax(s),  out = sum_t p_t v_t,  lse = log sum_t exp(s_t)
+//
+// Bound by the bytes of keys and values, each read once. The units of 128
+// tokens of all sequences and head tiles (16 query heads of one key-value
+// head) are shared out evenly over as many workgroups as the chip holds at
+// once (kv_plan.h), whatever the lengths, which only the device knows. A
+// workgroup walks its units; where it holds all of a sequence's units for a
+// head tile it writes the output, else a partial result (maximum, sum,
+// weighted values) that k_attend_join combines.
+//
+// A wave takes 32 of a unit's 128 tokens, on its own until its units end:
+//   S^T = K Q^T     tokens x heads, A = 16 rows of K as they lie in memory;
+//   O^T = V^T P^T   d x heads. The MFMA's layout puts a head's scores of 8
+//                   tokens into one lane, which are the 8 that the same lane
+//                   has to supply as the operand P^T: the weights never leave
+//                   their registers.
+// A lane loads E = DP / 16 neighbouring values of V for its 8 tokens, and
+// the A operand for d = E n + i (i < E) is the i-th of each: the transposition
+// is within a lane, one byte permutation for two values. Nothing goes through
+// LDS but 32 row numbers and scales for each 32 tokens.
+//
+// Precision. Products are of 16-bit operands, summed in fp32. int8 codes are
+// exact in bf16. An fp32 query is the sum of three bf16 or fp16 pieces (all 24
+// bits), an fp16 query on a bf16 or int8 cache of two; against an fp16 cache
+// other queries are first scaled by a power of two of the row's largest. The
+// weights are split in two pieces (2^-18 of a weight, below half a step of
+// the output), three for fp32 outputs on bf16 (fp16 weights are scaled by
+// 2^15 so that their second piece keeps them to 2^-22). Scores are in units of
+// log2 in fp32, where exp is v_exp_f32.
+#pragma once
+
+#include "paged_kv.h"
+
+namespace dq {
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kHeadTile = 16;  // query heads of a workgroup's item: the MFMA's columns
+
+struct AttendArgs {
+    DqAttendArgs a;
+    int q_type, Hq, Hk, D, cap, G, tiles;  // tiles: head tiles of a key-value head
+    int workers;
+    float* s;  // NULL: scores are not kept
+    size_t s_stride;
+    float* l2;    // [batch * Hq] log2 of the sum of exp
+    float* part;  // [workers][2][16][D + 4]: maximum, sum, -, -, weighted values
+    int32_t* bad;
+    KvGeom geom;
+};
+
+// A sequence's length, 0 where it is out of range (`bad` then).
+__device__ __forceinline__ int attend_len(const AttendArgs& A, int b, bool* bad) {
+    const int n = A.a.lens[b];
+    *bad = n < 0 || n > A.cap;
+    return *bad ? 0 : n;
+}
+
+__device__ __forceinline__ int64_t attend_units(const AttendArgs& A, int b) {
+    bool bad;
+    return (int64_t)kv_units(attend_len(A, b, &bad), A.a.window) * (A.Hk * A.tiles);
+}
+
+struct AttendScan {
+    int64_t sum[4];  // of each wave
+    int64_t base;
+    int b;
+};
+
+// All units of the batch, by a workgroup of 256 threads that take runs of
+// sequences; *mine is the number of units before this thread's run, *run its
+// length.
+__device__ __forceinline__ int64_t attend_scan(const AttendArgs& A, AttendScan* sh, int64_t* mine, int* run) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    *run = (A.a.batch + 255) / 256;
+    int64_t x = 0;
+    for (int i = 0; i < *run; ++i) {
+        const int b = tid * *run + i;
+        if (b < A.a.batch) x += attend_units(A, b);
+    }
+    int64_t y = x;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t z = __shfl_up(y, o);
+        if (lane >= o) y += z;
+    }
+    if (lane == 63) sh->sum[tid >> 6] = y;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < 4; ++w) {
+        if (w < (tid >> 6)) y += sh->sum[w];
+        total += sh->sum[w];
+    }
+    *mine = y - x;
+    return total;
+}
+
+// Workers that have a unit: a part is joined from consecutive ones.
+__device__ __forceinline__ int attend_workers(const AttendArgs& A, int64_t units) {
+    return (int)min((int64_t)A.workers, units);
+}
+
+// max and sum over the four lanes that hold one head (lane & 15)
+__device__ __forceinline__ float head_max(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float head_sum(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// a byte of a word as a signed value
+template <int I>
+__device__ __forceinline__ float code_f32(uint32_t w) {
+    return (float)((int32_t)(w << (24 - 8 * I)) >> 24);
+}
+// two fp32 values that are exact in bf16, as two bf16
+__device__ __forceinline__ uint32_t exact_bf16x2(float lo, float hi) {
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+// four int8 codes as four bf16
+__device__ __forceinline__ u2 codes_bf16x4(uint32_t w) {
+    const u2 r = {exact_bf16x2(code_f32<0>(w), code_f32<1>(w)), exact_bf16x2(code_f32<2>(w), code_f32<3>(w))};
+    return r;
+}
+
+template <int CT> struct AttendOps {  // bf16 products: bf16 and int8 caches
+    static constexpr float kOffset = 0.0f;
+    typedef __bf16 T;
+    static __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+    }
+};
+template <> struct AttendOps<DQ_F16> {
+    static constexpr float kOffset = 15.0f;  // weights are kept times 2^15
+    typedef _Float16 T;
+    static __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+    }
+};
+
+// eight fp32 values as NP pieces of T that add up to them
+template <typename T, int NP>
+__device__ __forceinline__ void pieces(const float (&x)[8], u4 (&out)[NP]) {
+    typedef T V __attribute__((ext_vector_type(8)));
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = x[j];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        V v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = (T)r[j];
+            r[j] -= (float)v[j];
+        }
+        out[p] = __builtin_bit_cast(u4, v);
+    }
+}
+
+// CT: the cache's type; NQ, NP: pieces of queries and weights; DP: the head
+// size rounded up to 64, 128 or 256; FULL: it is that size.
+template <int CT, int NQ, int NP, int DP, bool FULL>
+__global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendArgs A) {
+    typedef AttendOps<CT> Ops;
+    typedef typename Ops::T T;
+    constexpr int EB = CT == DQ_I8 ? 1 : 2;       // bytes of a value
+    constexpr int E = DP / 16;                    // values of V a lane loads for a token
+    constexpr int VW = E * EB / 4;                // their words
+    constexpr int C = DP / 32;                    // steps of 32 of q . k
+    constexpr int KL = DP * EB / 64;              // 16-byte loads of K for 16 tokens
+    constexpr int kAcc = DP + 4;
+    __shared__ AttendScan scan;
+    __shared__ int32_t s_row[4][32];
+    __shared__ float s_scale[4][64];
+    __shared__ float j_max[4][16], j_sum[4][16];
+    __shared__ float j_acc[4][16 * kAcc];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int n16 = lane & 15, g = lane >> 4;
+    const int D = A.D, row_bytes = D * EB;
+    const int items = A.Hk * A.tiles;
+
+    // ---- this workgroup's units
+    int64_t mine;
+    int run;
+    const int64_t units = attend_scan(A, &scan, &mine, &run);
+    // sequences without a token
+    for (int b = blockIdx.x; b < A.a.batch; b += A.workers) {
+        bool bad;
+        if (attend_len(A, b, &bad) > 0) continue;
+        if (bad && tid == 0) atomicAdd(A.bad, 1);
+        const float o = bad ? __builtin_nanf("") : 0.0f, l2 = bad ? __builtin_nanf("") : -__builtin_inff();
+        for (int i = tid; i < A.Hq * D; i += 256) store_any(A.a.out, A.q_type, (long long)b * A.Hq * D + i, o);
+        for (int i = tid; i < A.Hq; i += 256) {
+            A.l2[(size_t)b * A.Hq + i] = l2;
+            if (A.a.lse) A.a.lse[(size_t)b * A.Hq + i] = l2;
+        }
+    }
+    const int workers = attend_workers(A, units);
+    if ((int)blockIdx.x >= workers) return;
+    int64_t u = kv_first(blockIdx.x, workers, units);
+    const int64_t u_end = kv_first(blockIdx.x + 1, workers, units);
+    {
+        int64_t x = mine;
+        for (int i = 0; i < run; ++i) {
+            const int b = tid * run + i;
+            if (b >= A.a.batch) break;
+            const int64_t nb = attend_units(A, b);
+            if (u >= x && u < x + nb) {
+                scan.b = b;
+                scan.base = x;
+            }
+            x += nb;
+        }
+    }
+    __syncthreads();
+    int b = scan.b;
+    int64_t base = scan.base;
+
+    while (u < u_end) {
+        bool bad_len;
+        const int len = attend_len(A, b, &bad_len);
+        const int first = kv_first_token(len, A.a.window), nb = kv_units(len, A.a.window);
+        if (u >= base + (int64_t)nb * items) {
+            base += (int64_t)nb * items;
+            ++b;
+            continue;
+        }
+        const int item = (int)((u - base) / nb);
+        const int64_t item_u = base + (int64_t)item * nb;
+        const int unit0 = (int)(u - item_u);
+        const int count = (int)(min(u_end, item_u + nb) - u);
+        const int hk = item / A.tiles, h0 = hk * A.G + (item - hk * A.tiles) * kHeadTile;
+        const int heads = min(kHeadTile, (hk + 1) * A.G - h0);
+        const int32_t* line = A.a.table + (size_t)b * A.geom.per_seq;
+        const int t_end = min(len, first + (unit0 + count) * kKvUnit);
+        int t0 = first + unit0 * kKvUnit + wave * 32;
+
+        // ---- queries: head n16, the values of d that this lane's rows of K have
+        u4 q[C][NQ];
+        float scale = A.a.sm_scale * kLog2e;
+        {
+            const long long at = (long long)b * A.a.q_ts + (long long)(h0 + min(n16, heads - 1)) * A.a.q_hs;
+            float x[C][8];
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int d0 = CT == DQ_I8 ? (c >> 1) * 64 + g * 16 + (c & 1) * 8 : c * 32 + g * 8;
+                const bool in = n16 < heads && (FULL || d0 < D);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[c][j] = in ? load_any(A.a.q, A.q_type, at + d0 + j) : 0.0f;
+                    top = __builtin_fmaxf(top, __builtin_fabsf(x[c][j]));
+                }
+            }
+            if (CT == DQ_F16 && A.q_type != DQ_F16) {
+                // to [2^14, 2^15): the power of two of the row's largest
+                top = head_max(top);
+                const int e = top > 0.0f && top < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[c][j] = __builtin_ldexpf(x[c][j], e);
+                scale = __builtin_ldexpf(scale, -e);
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) pieces<T, NQ>(x[c], q[c]);
+        }
+
+        f4 acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
+        float m = -__builtin_inff(), l = 0.0f;
+        bool lost = false;
+
+        // the row of token t0 + (lane & 31) and, for an int8 cache, the scale
+        // of its key (lanes below 32) or value; a token past the end stands
+        // for the last one and is masked below
+        auto row_of = [&](int t) {
+            const int32_t r = kv_row(line, (uint32_t)min(t + (lane & 31), t_end - 1), hk, A.geom);
+            lost = lost || r < 0;
+            return max(r, 0);
+        };
+        u4 kf[2][KL];
+        auto load_k = [&](int32_t r0, int32_t r1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char* p = (const char*)A.a.k + (size_t)(uint32_t)(h ? r1 : r0) * row_bytes;
+#pragma unroll
+                for (int c = 0; c < KL; ++c) {
+                    const int o = c * 64 + g * 16;
+                    kf[h][c] = *(const u4*)(p + (FULL || o < row_bytes ? o : 0));
+                }
+            }
+        };
+        float sc = 0.0f;
+        if (t0 < t_end) {
+            const int32_t r = row_of(t0);
+            if (CT == DQ_I8) sc = (lane < 32 ? A.a.ks : A.a.vs)[r];
+            s_row[wave][lane & 31] = r;
+            wave_lds_fence();
+            load_k(s_row[wave][n16], s_row[wave][16 + n16]);
+        }
+        for (; t0 < t_end; t0 += 4 * 32) {
+            // rows of V, tokens 4 g + j and 16 + 4 g + j
+            const v4i ra = *(const v4i*)&s_row[wave][4 * g], rb = *(const v4i*)&s_row[wave][16 + 4 * g];
+            f4 ks[2], vs[2];
+            if (CT == DQ_I8) {
+                s_scale[wave][lane] = sc;
+                wave_lds_fence();
+                ks[0] = *(const f4*)&s_scale[wave][4 * g];
+                ks[1] = *(const f4*)&s_scale[wave][16 + 4 * g];
+                vs[0] = *(const f4*)&s_scale[wave][32 + 4 * g];
+                vs[1] = *(const f4*)&s_scale[wave][48 + 4 * g];
+            }
+            uint32_t vf[8][VW];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int32_t r = j < 4 ? ra[j] : rb[j - 4];
+                const int o = n16 * E * EB;
+                const char* p = (const char*)A.a.v + (size_t)(uint32_t)r * row_bytes + (FULL || o < row_bytes ? o : 0);
+                typedef uint32_t W __attribute__((ext_vector_type(VW < 4 ? VW : 4)));
+                if constexpr (VW == 1) {
+                    vf[j][0] = *(const uint32_t*)p;
+                } else {
+#pragma unroll
+                    for (int w = 0; w < VW; w += 4) {
+                        const W x = *(const W*)(p + 4 * w);
+#pragma unroll
+                        for (int i = 0; i < (VW < 4 ? VW : 4); ++i) vf[j][w + i] = x[i];
+                    }
+                }
+            }
+            issue_fence();
+            // ---- scores
+            f4 s[2] = {f4{0, 0, 0, 0}, f4{0, 0, 0, 0}};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < KL; ++c) {
+                    u4 x = kf[h][c];
+                    if (!FULL && c * 64 + g * 16 >= row_bytes) x = u4{0, 0, 0, 0};
+                    if constexpr (CT == DQ_I8) {
+                        const u2 a = codes_bf16x4(x[0]), e = codes_bf16x4(x[1]), i = codes_bf16x4(x[2]),
+                                 o = codes_bf16x4(x[3]);
+#pragma unroll
+                        for (int p = 0; p < NQ; ++p) {
+                            s[h] = Ops::mfma(u4{a[0], a[1], e[0], e[1]}, q[2 * c][p], s[h]);
+                            s[h] = Ops::mfma(u4{i[0], i[1], o[0], o[1]}, q[2 * c + 1][p], s[h]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < NQ; ++p) s[h] = Ops::mfma(x, q[c][p], s[h]);
+                    }
+                }
+            // ---- next keys
+            const int t1 = t0 + 4 * 32;
+            if (t1 < t_end) {
+                const int32_t r = row_of(t1);
+                if (CT == DQ_I8) sc = (lane < 32 ? A.a.ks : A.a.vs)[r];
+                s_row[wave][lane & 31] = r;
+                wave_lds_fence();
+                load_k(s_row[wave][n16], s_row[wave][16 + n16]);
+            }
+            issue_fence();
+            // ---- weights
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float y = s[j >> 2][j & 3];
+                if (CT == DQ_I8) y *= ks[j >> 2][j & 3];
+                y *= scale;
+                x[j] = t0 + 16 * (j >> 2) + 4 * g + (j & 3) < t_end ? y : -__builtin_inff();
+            }
+            if (A.s && n16 < heads) {
+                float* o = A.s + (size_t)(b * A.Hq + h0 + n16) * A.s_stride + (t0 - first) + 4 * g;
+                *(f4*)o = f4{x[0], x[1], x[2], x[3]};
+                *(f4*)(o + 16) = f4{x[4], x[5], x[6], x[7]};
+            }
+            float top = x[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[j]);
+            top = __builtin_fmaxf(head_max(top) - Ops::kOffset, m);
+            const float ref = top == -__builtin_inff() ? 0.0f : top;
+            if (__ballot(top != m)) {
+                const float f = __builtin_amdgcn_exp2f(m - ref);
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[i] *= f;
+                m = top;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = __builtin_amdgcn_exp2f(x[j] - ref);
+                l += x[j];
+                if (CT == DQ_I8) x[j] *= vs[j >> 2][j & 3];
+            }
+            if (t0 + 32 > t_end) {
+                // the tokens that stand in past the end: their weight is 0, but
+                // 0 times what is not finite would not be
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (t0 + 16 * (j >> 2) + 4 * g + (j & 3) >= t_end) {
+                        x[j] = 0.0f;
+#pragma unroll
+                        for (int w = 0; w < VW; ++w) vf[j][w] = 0;
+                    }
+            }
+            u4 p[NP];
+            pieces<T, NP>(x, p);
+            // ---- values: operand i has value i of each of the lane's tokens
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                u4 a;
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    if constexpr (CT == DQ_I8) {
+                        const uint32_t x0 = vf[2 * jj][i >> 2] << (24 - 8 * (i & 3));
+                        const uint32_t x1 = vf[2 * jj + 1][i >> 2] << (24 - 8 * (i & 3));
+                        a[jj] = exact_bf16x2((float)((int32_t)x0 >> 24), (float)((int32_t)x1 >> 24));
+                    } else {
+                        a[jj] = __builtin_amdgcn_perm(vf[2 * jj + 1][i >> 1], vf[2 * jj][i >> 1],
+                                                      i & 1 ? 0x07060302u : 0x05040100u);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < NP; ++w) acc[i] = Ops::mfma(a, p[w], acc[i]);
+            }
+        }
+
+        // ---- the four waves' results
+        l = head_sum(l);
+        if (__ballot(lost)) {
+            l = __builtin_nanf("");
+            if (lane == 0) atomicAdd(A.bad, 1);
+        }
+        if (g == 0) {
+            j_max[wave][n16] = m;
+            j_sum[wave][n16] = l;
+        }
+        if (n16 < heads) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < E; i += 4)
+                    *(f4*)&j_acc[wave][n16 * kAcc + E * (4 * g + r) + i] =
+                        f4{acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]};
+        }
+        __syncthreads();
+        const bool whole = unit0 == 0 && count == nb;
+        float* part = A.part + (size_t)(2 * blockIdx.x + (unit0 == 0 ? 1 : 0)) * kHeadTile * (D + 4);
+        for (int e = tid; e < heads * (D / 4); e += 256) {
+            const int n = e / (D / 4), d = (e - n * (D / 4)) * 4;
+            float top = j_max[0][n];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) top = __builtin_fmaxf(top, j_max[w][n]);
+            const float ref = top == -__builtin_inff() ? 0.0f : top;
+            float sum = 0.0f;
+            f4 o = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = __builtin_amdgcn_exp2f(j_max[w][n] - ref);
+                sum += j_sum[w][n] * f;
+                o += *(const f4*)&j_acc[w][n * kAcc + d] * f;
+            }
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const size_t i = (size_t)b * A.Hq + h0 + n;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    store_any(A.a.out, A.q_type, (long long)(i * D + d + k), sum == 0.0f ? 0.0f : o[k] * inv);
+                if (d == 0) {
+                    const float l2 = sum == 0.0f ? -__builtin_inff() : ref + __builtin_amdgcn_logf(sum);
+                    A.l2[i] = l2;
+                    if (A.a.lse) A.a.lse[i] = l2 * kLn2;
+                }
+            } else {
+                *(f4*)&part[n * (D + 4) + 4 + d] = o;
+                if (d == 0) {
+                    part[n * (D + 4)] = top;
+                    part[n * (D + 4) + 1] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        u += count;
+    }
+}
+
+// instances of one cache type (paged_attend_*.hip)
+typedef void (*AttendKernel)(const AttendArgs);
+AttendKernel attend_bf16(dq_dtype q, int D);
+AttendKernel attend_f16(dq_dtype q, int D);
+AttendKernel attend_i8(dq_dtype q, int D);
+
+template <int CT, int NQ, int NP>
+AttendKernel attend_pick(int D) {
+    if (D <= 64) return D == 64 ? k_attend<CT, NQ, NP, 64, true> : k_attend<CT, NQ, NP, 64, false>;
+    if (D <= 128) return D == 128 ? k_attend<CT, NQ, NP, 128, true> : k_attend<CT, NQ, NP, 128, false>;
+    return D == 256 ? k_attend<CT, NQ, NP, 256, true> : k_attend<CT, NQ, NP, 256, false>;
+}
+
+}  // namespace dq

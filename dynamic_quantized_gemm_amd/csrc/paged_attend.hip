@@ -1,137 +1,140 @@
 // paged_attend.hip -- attention of one new token of every sequence over the
-// paged key-value cache.
-//
-//   s_t = sm_scale q . k_t     for the tokens t in [max(0, len - window), len)
-//   p   = softmax(s),  out = sum_t p_t v_t,  lse = log sum_t exp(s_t)
-// and, where weights are gathered, scores' = decay scores + sum of p_t over
-// the query heads of a key-value head.
-//
-// One workgroup for a sequence and a query head: each wave takes every fourth
-// token, with a running maximum and sum, and the waves are joined in LDS.
-// Scores are kept in units of log2 (s log2 e), so that exp is v_exp_f32.
-#include "paged_kv.h"
+// paged key-value cache: the join of partial results, the gathered weights,
+// and the launches. The attention itself is in attend_kernel.h.
+#include <algorithm>
+
+#include "attend_kernel.h"
 
 using namespace dq;
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-
-struct SimpleArgs {
-    DqAttendArgs a;
-    int q_type, cache_type, Hq, Hk, D, cap;
-    float* s;
-    size_t s_stride;
-    float* l2;  // [batch * Hq] log2 of the sum
-    int32_t* bad;
-    KvGeom geom;
-};
-
-__device__ __forceinline__ float wave_sum(float v) {
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
-}
-
-__device__ __forceinline__ int seq_len(const int32_t* lens, int b, int cap, bool* bad) {
-    const int n = lens[b];
-    *bad = n < 0 || n > cap;
-    return n < 0 ? 0 : min(n, cap);
-}
-
-__global__ void __launch_bounds__(256) k_attend(const SimpleArgs A) {
-    __shared__ float sm[4], sl[4], sacc[4][256];
-    const int hq = blockIdx.x, b = blockIdx.y, hk = hq / (A.Hq / A.Hk);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    bool bad;
-    const int n = seq_len(A.a.lens, b, A.cap, &bad);
-    if (bad && threadIdx.x == 0) atomicAdd(A.bad, 1);
-    const int first = kv_first_token(n, A.a.window);
-    const int32_t* line = A.a.table + (size_t)b * A.geom.per_seq;
-    float q[4], acc[4] = {0, 0, 0, 0}, m = -__builtin_inff(), l = 0.0f;
-    for (int j = 0; j < 4; ++j) {
-        const int d = lane + 64 * j;
-        q[j] = d < A.D ? load_any(A.a.q, A.q_type, b * A.a.q_ts + hq * A.a.q_hs + d) : 0.0f;
+// Joins the partial results of a query head whose units several workgroups
+// took: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i. One workgroup a head;
+// groups of D / 4 lanes take the parts in turn and are added in order in LDS,
+// so a result never depends on timing.
+__global__ void __launch_bounds__(256) k_attend_join(const AttendArgs A) {
+    __shared__ AttendScan scan;
+    __shared__ float s_top[4], s_sum[16];
+    __shared__ f4 s_acc[256];
+    const int tid = threadIdx.x, h = blockIdx.x, b = blockIdx.y;
+    int64_t mine;
+    int run;
+    const int64_t units = attend_scan(A, &scan, &mine, &run);
+    if (tid == b / run) {
+        for (int i = tid * run; i < b; ++i) mine += attend_units(A, i);
+        scan.base = mine;
     }
-    for (int t = first + wave; t < n; t += 4) {
-        int32_t row = kv_row(line, (uint32_t)t, hk, A.geom);
-        const bool lost = row < 0;
-        if (lost) {
-            if (lane == 0) atomicAdd(A.bad, 1);
-            row = 0;
-        }
-        float x = 0.0f;
-        for (int j = 0; j < 4; ++j) {
-            const int d = lane + 64 * j;
-            if (d < A.D) x += q[j] * load_any(A.a.k, A.cache_type, (long long)row * A.D + d);
-        }
-        x = wave_sum(x);
-        if (A.a.ks) x *= A.a.ks[row];
-        x *= A.a.sm_scale * kLog2e;
-        if (lost) x = __builtin_nanf("");
-        if (A.a.scores && lane == 0) A.s[(size_t)(b * A.Hq + hq) * A.s_stride + (t - first)] = x;
-        const float m1 = __builtin_fmaxf(m, x);
-        const float ref = m1 == -__builtin_inff() ? 0.0f : m1;
-        const float f = __builtin_amdgcn_exp2f(m - ref), p = __builtin_amdgcn_exp2f(x - ref);
-        const float w = A.a.vs ? p * A.a.vs[row] : p;
-        l = l * f + p;
-        for (int j = 0; j < 4; ++j) {
-            const int d = lane + 64 * j;
-            if (d < A.D) acc[j] = acc[j] * f + w * load_any(A.a.v, A.cache_type, (long long)row * A.D + d);
-        }
-        m = m1;
-    }
-    if (lane == 0) {
-        sm[wave] = m;
-        sl[wave] = l;
-    }
-    for (int j = 0; j < 4; ++j) sacc[wave][lane + 64 * j] = acc[j];
     __syncthreads();
-    float top = __builtin_fmaxf(__builtin_fmaxf(sm[0], sm[1]), __builtin_fmaxf(sm[2], sm[3]));
+    bool bad;
+    const int len = attend_len(A, b, &bad), nb = kv_units(len, A.a.window);
+    if (nb == 0) return;
+    const int hk = h / A.G, x = h - hk * A.G;
+    const int64_t first_u = scan.base + (int64_t)(hk * A.tiles + x / kHeadTile) * nb;
+    const int workers = attend_workers(A, units);
+    const int w0 = kv_worker(first_u, workers, units), w1 = kv_worker(first_u + nb - 1, workers, units);
+    if (w0 == w1) return;
+    const int stride = kHeadTile * (A.D + 4), parts = w1 - w0 + 1;
+    // the first worker's part began with the head's first unit: its second
+    // slot; the others' is their first
+    const float* base = A.part + (size_t)2 * w0 * stride + (size_t)(x % kHeadTile) * (A.D + 4);
+    auto part = [&](int i) { return base + (size_t)(2 * i + (i == 0)) * stride; };
+    float top = -__builtin_inff();
+    for (int i = tid; i < parts; i += 256) top = __builtin_fmaxf(top, part(i)[0]);
+    top = wave_max_uniform(top);
+    if ((tid & 63) == 0) s_top[tid >> 6] = top;
+    __syncthreads();
+    top = __builtin_fmaxf(__builtin_fmaxf(s_top[0], s_top[1]), __builtin_fmaxf(s_top[2], s_top[3]));
     const float ref = top == -__builtin_inff() ? 0.0f : top;
-    float sum = 0.0f, o = 0.0f;
-    const int d = threadIdx.x;
-    for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sm[w] - ref);
-        sum += sl[w] * f;
-        o += sacc[w][d] * f;
+    const int lanes = A.D / 4, groups = min(16, 256 / lanes), grp = tid / lanes, d = tid - grp * lanes;
+    float sum = 0.0f;
+    f4 o = {0, 0, 0, 0};
+    if (grp < groups) {
+        for (int i = grp; i < parts; i += groups) {
+            const float* p = part(i);
+            const float f = __builtin_amdgcn_exp2f(p[0] - ref);
+            sum += p[1] * f;
+            o += *(const f4*)(p + 4 + 4 * d) * f;
+        }
+        s_acc[tid] = o;
+        if (d == 0) s_sum[grp] = sum;
     }
-    o = sum == 0.0f ? 0.0f : o / sum;
-    float l2 = sum == 0.0f ? -__builtin_inff() : ref + __builtin_amdgcn_logf(sum);
-    if (bad) o = l2 = __builtin_nanf("");
-    const size_t i = (size_t)b * A.Hq + hq;
-    if (d < A.D) store_any(A.a.out, A.q_type, (long long)(i * A.D + d), o);
+    __syncthreads();
+    if (grp > 0) return;
+    sum = 0.0f;
+    o = f4{0, 0, 0, 0};
+    for (int i = 0; i < groups; ++i) {
+        sum += s_sum[i];
+        o += s_acc[i * lanes + d];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const size_t i = (size_t)b * A.Hq + h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        store_any(A.a.out, A.q_type, (long long)(i * A.D + 4 * d + k), sum == 0.0f ? 0.0f : o[k] * inv);
     if (d == 0) {
+        const float l2 = sum == 0.0f ? -__builtin_inff() : ref + __builtin_amdgcn_logf(sum);
         A.l2[i] = l2;
         if (A.a.lse) A.a.lse[i] = l2 * kLn2;
     }
 }
 
-__global__ void __launch_bounds__(256) k_gather_scores(const SimpleArgs A) {
-    const int item = blockIdx.y, b = item / A.Hk, hk = item - b * A.Hk, G = A.Hq / A.Hk;
+// scores' = decay scores + the sum of 2^(s - l2) over a key-value head's heads
+__global__ void __launch_bounds__(256) k_gather_scores(const AttendArgs A) {
+    const int item = blockIdx.y, b = item / A.Hk, hk = item - b * A.Hk;
     bool bad;
-    const int n = seq_len(A.a.lens, b, A.cap, &bad), first = kv_first_token(n, A.a.window);
+    const int n = attend_len(A, b, &bad), first = kv_first_token(n, A.a.window);
     for (int t = blockIdx.x * 256 + threadIdx.x; t < n; t += gridDim.x * 256) {
-        float sum = A.a.scores[(size_t)item * A.cap + t] * A.a.decay;
         float p = 0.0f;
         if (t >= first)
-            for (int g = 0; g < G; ++g) {
-                const size_t i = (size_t)b * A.Hq + hk * G + g;
+            for (int g = 0; g < A.G; ++g) {
+                const size_t i = (size_t)b * A.Hq + hk * A.G + g;
                 const float l2 = A.l2[i];
                 if (l2 != -__builtin_inff()) p += __builtin_amdgcn_exp2f(A.s[i * A.s_stride + (t - first)] - l2);
             }
-        A.a.scores_out[(size_t)item * A.cap + t] = sum + p;
+        const size_t at = (size_t)item * A.cap + t;
+        A.a.scores_out[at] = A.a.scores[at] * A.a.decay + p;
     }
 }
 
+constexpr int kPerCu = 2;  // workgroups of k_attend on a compute unit
+
+int max_workers(const dq_kv_ctx* c) { return c->cus * kPerCu; }
+
 }  // namespace
 
-size_t dq_attend_part_floats(const dq_kv_ctx* c) { return (size_t)c->batch * c->Hq; }
+size_t dq_attend_part_floats(const dq_kv_ctx* c) {
+    return (size_t)c->batch * c->Hq + 3 + (size_t)max_workers(c) * 2 * kHeadTile * (c->D + 4);
+}
 
 int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s) {
-    const SimpleArgs A{a, c->q_type, c->cache_type, c->Hq, c->Hk, c->D, c->cap, c->s, c->s_stride, c->part, c->bad,
-                       c->geom};
-    hipLaunchKernelGGL(k_attend, dim3((unsigned)c->Hq, (unsigned)a.batch), dim3(256), 0, s, A);
+    AttendArgs A{};
+    A.a = a;
+    A.q_type = c->q_type;
+    A.Hq = c->Hq;
+    A.Hk = c->Hk;
+    A.D = c->D;
+    A.cap = c->cap;
+    A.G = c->Hq / c->Hk;
+    A.tiles = (A.G + kHeadTile - 1) / kHeadTile;
+    A.s = a.scores ? c->s : nullptr;
+    A.s_stride = c->s_stride;
+    A.part = c->part;
+    A.l2 = c->part + (size_t)max_workers(c) * 2 * kHeadTile * (c->D + 4);
+    A.bad = c->bad;
+    A.geom = c->geom;
+    // as many workers as the most units that the call can have, up to the chip's
+    const int64_t per_item = kv_units(c->cap, a.window);
+    const int64_t most = per_item * a.batch * A.Hk * A.tiles;
+    A.workers = (int)std::min<int64_t>(most, max_workers(c));
+    const AttendKernel k = c->cache_type == DQ_I8 ? attend_i8(c->q_type, c->D)
+                           : c->cache_type == DQ_F16 ? attend_f16(c->q_type, c->D) : attend_bf16(c->q_type, c->D);
+    hipLaunchKernelGGL(k, dim3((unsigned)A.workers), dim3(256), 0, s, A);
     DQ_LAUNCH_CHECK("attention");
+    if (per_item > 1) {
+        hipLaunchKernelGGL(k_attend_join, dim3((unsigned)c->Hq, (unsigned)a.batch), dim3(256), 0, s, A);
+        DQ_LAUNCH_CHECK("join of the attention's parts");
+    }
     if (a.scores) {
         hipLaunchKernelGGL(k_gather_scores, dim3((unsigned)((c->cap + 1023) / 1024), (unsigned)(a.batch * c->Hk)),
                            dim3(256), 0, s, A);

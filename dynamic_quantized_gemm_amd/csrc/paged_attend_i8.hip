@@ -1,0 +1,15 @@
+// paged_attend_i8.hip -- the attention kernel's instances for this cache type
+// (attend_kernel.h).
+#include "attend_kernel.h"
+
+namespace dq {
+
+// pieces of bf16: a bf16 query is one, an fp16 one (11 digits) two, an fp32
+// one three; fp32 outputs keep the weights in three pieces
+AttendKernel attend_i8(dq_dtype q, int D) {
+    if (q == DQ_F32) return attend_pick<DQ_I8, 3, 3>(D);
+    if (q == DQ_F16) return attend_pick<DQ_I8, 2, 2>(D);
+    return attend_pick<DQ_I8, 1, 2>(D);
+}
+
+}  // namespace dq
