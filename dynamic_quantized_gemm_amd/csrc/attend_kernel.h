@@ -47,8 +47,9 @@ struct AttendArgs {
     DqAttendArgs a;
     int q_type, Hq, Hk, D, cap, G, tiles;  // tiles: head tiles of a key-value head
     int workers;
-    float* s;  // NULL: scores are not kept
-    size_t s_stride;
+    int q_vec;  // queries can be loaded 16 bytes at a time
+    float* s;         // NULL: scores are not kept; else for each key-value head
+    size_t s_stride;  // (s_stride apart), runs of 32 tokens: [G][32]
     float* l2;    // [batch * Hq] log2 of the sum of exp
     float* part;  // [workers][2][16][D + 4]: maximum, sum, -, -, weighted values
     int32_t* bad;
@@ -103,6 +104,18 @@ __device__ __forceinline__ int64_t attend_scan(const AttendArgs& A, AttendScan* 
 // Workers that have a unit: a part is joined from consecutive ones.
 __device__ __forceinline__ int attend_workers(const AttendArgs& A, int64_t units) {
     return (int)min((int64_t)A.workers, units);
+}
+
+// The scores of a run of 32 tokens (from the window's first on) of a
+// key-value head: one piece of memory for all its query heads.
+__device__ __forceinline__ size_t attend_score_at(const AttendArgs& A, int item, int run) {
+    return (size_t)item * A.s_stride + (size_t)run * (32 * A.G);
+}
+
+// A value that is the same in all lanes, kept in scalar registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32 | (uint32_t)uniform((int)x));
 }
 
 // max and sum over the four lanes that hold one head (lane & 15)
@@ -171,7 +184,7 @@ __device__ __forceinline__ void pieces(const float (&x)[8], u4 (&out)[NP]) {
 // CT: the cache's type; NQ, NP: pieces of queries and weights; DP: the head
 // size rounded up to 64, 128 or 256; FULL: it is that size.
 template <int CT, int NQ, int NP, int DP, bool FULL>
-__global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendArgs A) {
+__global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8 && NQ == 1) ? 3 : 2) k_attend(const AttendArgs A) {
     typedef AttendOps<CT> Ops;
     typedef typename Ops::T T;
     constexpr int EB = CT == DQ_I8 ? 1 : 2;       // bytes of a value
@@ -186,7 +199,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
     __shared__ float j_max[4][16], j_sum[4][16];
     __shared__ float j_acc[4][16 * kAcc];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n16 = lane & 15, g = lane >> 4;
     const int D = A.D, row_bytes = D * EB;
     const int items = A.Hk * A.tiles;
@@ -194,7 +207,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
     // ---- this workgroup's units
     int64_t mine;
     int run;
-    const int64_t units = attend_scan(A, &scan, &mine, &run);
+    const int64_t units = uniform(attend_scan(A, &scan, &mine, &run));
     // sequences without a token
     for (int b = blockIdx.x; b < A.a.batch; b += A.workers) {
         bool bad;
@@ -207,7 +220,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
             if (A.a.lse) A.a.lse[(size_t)b * A.Hq + i] = l2;
         }
     }
-    const int workers = attend_workers(A, units);
+    const int workers = uniform(attend_workers(A, units));
     if ((int)blockIdx.x >= workers) return;
     int64_t u = kv_first(blockIdx.x, workers, units);
     const int64_t u_end = kv_first(blockIdx.x + 1, workers, units);
@@ -225,8 +238,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
         }
     }
     __syncthreads();
-    int b = scan.b;
-    int64_t base = scan.base;
+    int b = uniform(scan.b);
+    int64_t base = uniform(scan.base);
 
     while (u < u_end) {
         bool bad_len;
@@ -247,25 +260,108 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
         const int t_end = min(len, first + (unit0 + count) * kKvUnit);
         int t0 = first + unit0 * kKvUnit + wave * 32;
 
-        // ---- queries: head n16, the values of d that this lane's rows of K have
+        // ---- queries: head n16, the values of d that this lane's rows of K
+        // have; on their way while the first rows are looked up
+        constexpr int QW = NQ == 3 ? 8 : 4;  // words of eight values: fp32 or 16 bits
+        uint32_t raw[C][QW];
+        {
+            constexpr int QE = QW / 2;  // bytes of a value
+            const char* p = (const char*)A.a.q + ((long long)b * A.a.q_ts + (long long)(h0 + min(n16, heads - 1)) * A.a.q_hs) * QE;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int d0 = CT == DQ_I8 ? (c >> 1) * 64 + g * 16 + (c & 1) * 8 : c * 32 + g * 8;
+                const char* x = p + (FULL || d0 < D ? d0 : 0) * QE;
+                if (A.q_vec) {
+#pragma unroll
+                    for (int w = 0; w < QW; w += 4) {
+                        const u4 y = *(const u4*)(x + 4 * w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) raw[c][w + i] = y[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < QW; ++w)
+                        raw[c][w] = QE == 4 ? ((const uint32_t*)x)[w]
+                                            : ((const uint16_t*)x)[2 * w] | (uint32_t)((const uint16_t*)x)[2 * w + 1] << 16;
+                }
+            }
+        }
+        issue_fence();
+
+        f4 acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
+        float m = -__builtin_inff(), l = 0.0f;
+        bool lost = false;
+
+        // the block table's entry for token t + (lane & 31), and that token's row;
+        // a token past the end stands for the last one and is masked below
+        // (t_end is at most a sequence's slots, so the entry is in the table)
+        auto entry_of = [&](int t) { return line[kv_div((uint32_t)min(t + (lane & 31), t_end - 1), A.geom.page)]; };
+        auto row_of = [&](int t, int32_t page) {
+            const int32_t r = kv_row_of(page, (uint32_t)min(t + (lane & 31), t_end - 1), hk, A.geom);
+            lost = lost || r < 0;
+            return max(r, 0);
+        };
+        u4 kf[2][KL];
+        auto load_k = [&](int32_t r0, int32_t r1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char* p = (const char*)A.a.k + (size_t)(uint32_t)(h ? r1 : r0) * row_bytes;
+#pragma unroll
+                for (int c = 0; c < KL; ++c) {
+                    const int o = c * 64 + g * 16;
+                    kf[h][c] = __builtin_nontemporal_load((const u4*)(p + (FULL || o < row_bytes ? o : 0)));
+                }
+            }
+        };
+        // for an int8 cache, the scale of a token's key (lanes below 32) or value
+        const float* scales = CT == DQ_I8 ? (lane < 32 ? A.a.ks : A.a.vs) : nullptr;
+        float sc = 0.0f;
+        int32_t page1 = 0;
+        if (t0 < t_end) {
+            const int32_t page0 = entry_of(t0);
+            page1 = entry_of(t0 + 4 * 32);
+            const int32_t r = row_of(t0, page0);
+            if (CT == DQ_I8) sc = scales[r];
+            s_row[wave][lane & 31] = r;
+            wave_lds_fence();
+            load_k(s_row[wave][n16], s_row[wave][16 + n16]);
+        }
+        // kept scores go out as buffer stores, which drop the lanes without a
+        // head (and all, where none are kept): no branch around them
+        const auto s_out = __builtin_amdgcn_make_buffer_rsrc(
+            A.s + attend_score_at(A, b * A.Hk + hk, 0), 0, A.s ? (int)(A.s_stride * 4) : 0, 0x00027000);
+
+        // ---- queries as MFMA operands
         u4 q[C][NQ];
         float scale = A.a.sm_scale * kLog2e;
         {
-            const long long at = (long long)b * A.a.q_ts + (long long)(h0 + min(n16, heads - 1)) * A.a.q_hs;
             float x[C][8];
-            float top = 0.0f;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int d0 = CT == DQ_I8 ? (c >> 1) * 64 + g * 16 + (c & 1) * 8 : c * 32 + g * 8;
                 const bool in = n16 < heads && (FULL || d0 < D);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    x[c][j] = in ? load_any(A.a.q, A.q_type, at + d0 + j) : 0.0f;
-                    top = __builtin_fmaxf(top, __builtin_fabsf(x[c][j]));
+                    float y;
+                    if (NQ == 3) {
+                        y = __uint_as_float(raw[c][j % QW]);
+                    } else {
+                        const uint16_t h = (uint16_t)(raw[c][j / 2] >> (16 * (j & 1)));
+                        const bool half = NQ == 2 || (CT == DQ_F16 && A.q_type == DQ_F16);
+                        y = half ? (float)__builtin_bit_cast(_Float16, h) : bf16_bits_to_f32(h);
+                    }
+                    x[c][j] = in ? y : 0.0f;
                 }
             }
             if (CT == DQ_F16 && A.q_type != DQ_F16) {
                 // to [2^14, 2^15): the power of two of the row's largest
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, __builtin_fabsf(x[c][j]));
                 top = head_max(top);
                 const int e = top > 0.0f && top < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
 #pragma unroll
@@ -278,41 +374,11 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
             for (int c = 0; c < C; ++c) pieces<T, NQ>(x[c], q[c]);
         }
 
-        f4 acc[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = f4{0, 0, 0, 0};
-        float m = -__builtin_inff(), l = 0.0f;
-        bool lost = false;
-
-        // the row of token t0 + (lane & 31) and, for an int8 cache, the scale
-        // of its key (lanes below 32) or value; a token past the end stands
-        // for the last one and is masked below
-        auto row_of = [&](int t) {
-            const int32_t r = kv_row(line, (uint32_t)min(t + (lane & 31), t_end - 1), hk, A.geom);
-            lost = lost || r < 0;
-            return max(r, 0);
-        };
-        u4 kf[2][KL];
-        auto load_k = [&](int32_t r0, int32_t r1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const char* p = (const char*)A.a.k + (size_t)(uint32_t)(h ? r1 : r0) * row_bytes;
-#pragma unroll
-                for (int c = 0; c < KL; ++c) {
-                    const int o = c * 64 + g * 16;
-                    kf[h][c] = *(const u4*)(p + (FULL || o < row_bytes ? o : 0));
-                }
-            }
-        };
-        float sc = 0.0f;
-        if (t0 < t_end) {
-            const int32_t r = row_of(t0);
-            if (CT == DQ_I8) sc = (lane < 32 ? A.a.ks : A.a.vs)[r];
-            s_row[wave][lane & 31] = r;
-            wave_lds_fence();
-            load_k(s_row[wave][n16], s_row[wave][16 + n16]);
-        }
+        // Loads return in order and a wait names how many may be outstanding, so
+        // no load or store of the loop is behind a branch: an iteration's
+        // values are waited for while the next one's keys are on their way.
         for (; t0 < t_end; t0 += 4 * 32) {
+            const int32_t page2 = entry_of(t0 + 2 * 4 * 32);
             // rows of V, tokens 4 g + j and 16 + 4 g + j
             const v4i ra = *(const v4i*)&s_row[wave][4 * g], rb = *(const v4i*)&s_row[wave][16 + 4 * g];
             f4 ks[2], vs[2];
@@ -332,11 +398,11 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
                 const char* p = (const char*)A.a.v + (size_t)(uint32_t)r * row_bytes + (FULL || o < row_bytes ? o : 0);
                 typedef uint32_t W __attribute__((ext_vector_type(VW < 4 ? VW : 4)));
                 if constexpr (VW == 1) {
-                    vf[j][0] = *(const uint32_t*)p;
+                    vf[j][0] = __builtin_nontemporal_load((const uint32_t*)p);
                 } else {
 #pragma unroll
                     for (int w = 0; w < VW; w += 4) {
-                        const W x = *(const W*)(p + 4 * w);
+                        const W x = __builtin_nontemporal_load((const W*)(p + 4 * w));
 #pragma unroll
                         for (int i = 0; i < (VW < 4 ? VW : 4); ++i) vf[j][w + i] = x[i];
                     }
@@ -364,16 +430,6 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
                         for (int p = 0; p < NQ; ++p) s[h] = Ops::mfma(x, q[c][p], s[h]);
                     }
                 }
-            // ---- next keys
-            const int t1 = t0 + 4 * 32;
-            if (t1 < t_end) {
-                const int32_t r = row_of(t1);
-                if (CT == DQ_I8) sc = (lane < 32 ? A.a.ks : A.a.vs)[r];
-                s_row[wave][lane & 31] = r;
-                wave_lds_fence();
-                load_k(s_row[wave][n16], s_row[wave][16 + n16]);
-            }
-            issue_fence();
             // ---- weights
             float x[8];
 #pragma unroll
@@ -383,11 +439,24 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attend(const AttendA
                 y *= scale;
                 x[j] = t0 + 16 * (j >> 2) + 4 * g + (j & 3) < t_end ? y : -__builtin_inff();
             }
-            if (A.s && n16 < heads) {
-                float* o = A.s + (size_t)(b * A.Hq + h0 + n16) * A.s_stride + (t0 - first) + 4 * g;
-                *(f4*)o = f4{x[0], x[1], x[2], x[3]};
-                *(f4*)(o + 16) = f4{x[4], x[5], x[6], x[7]};
+            {
+                const int o = (((t0 - first) >> 5) * A.G + (h0 - hk * A.G + n16)) * 32 + 4 * g;
+                const int at = n16 < heads ? o * 4 : -256;
+                const f4 y0 = {x[0], x[1], x[2], x[3]}, y1 = {x[4], x[5], x[6], x[7]};
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y0), s_out, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, y1), s_out, at + 64, 0, 0);
             }
+            // ---- next keys; past the end, the last row once more
+            {
+                const int32_t r = row_of(t0 + 4 * 32, page1);
+                page1 = page2;
+                if (CT == DQ_I8) sc = scales[r];
+                s_row[wave][lane & 31] = r;
+                wave_lds_fence();
+                load_k(s_row[wave][n16], s_row[wave][16 + n16]);
+            }
+            issue_fence();
+            // ---- the running maximum
             float top = x[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[j]);

@@ -43,14 +43,16 @@ struct KvGeom {
 
 // Row (of D values) of token t of a sequence for key-value head h, where table
 // is the sequence's line of the block table; -1 where t lies beyond the table
-// or its entry names no page. The largest row fits 31 bits (checked when a
+// or its entry names no page (kv_row_of: given the entry). The largest row fits 31 bits (checked when a
 // context is made); byte offsets are taken from it in 64 bits.
+DQ_HD int32_t kv_row_of(int32_t entry, uint32_t t, int h, const KvGeom& g) {
+    const uint32_t p = (uint32_t)entry;
+    if (p >= (uint32_t)g.pages) return -1;
+    return (int32_t)((p * (uint32_t)g.heads + (uint32_t)h) * g.page.d + (t - kv_div(t, g.page) * g.page.d));
+}
 DQ_HD int32_t kv_row(const int32_t* table, uint32_t t, int h, const KvGeom& g) {
     const uint32_t e = kv_div(t, g.page);
-    if (e >= (uint32_t)g.per_seq) return -1;
-    const uint32_t p = (uint32_t)table[e];
-    if (p >= (uint32_t)g.pages) return -1;
-    return (int32_t)((p * (uint32_t)g.heads + (uint32_t)h) * g.page.d + (t - e * g.page.d));
+    return e < (uint32_t)g.per_seq ? kv_row_of(table[e], t, h, g) : -1;
 }
 
 // The two elements of virtual pair i of a row of D elements, the first R of

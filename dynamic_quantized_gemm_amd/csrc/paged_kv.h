@@ -26,10 +26,11 @@ struct dq_kv_ctx {
     int32_t* moves = nullptr;  // eviction: [batch * Hk] counts, then per head the slots
                                // freed and those moved into them
     size_t moves_stride = 0;
-    float* s = nullptr;        // [batch * Hq, s_stride] scores of the attention (log2)
+    float* s = nullptr;        // [batch * Hk, s_stride] scores of the attention (log2)
     size_t s_stride = 0;
     float* part = nullptr;     // partial results of the attention
     size_t part_floats = 0;
+    int attend_workers = 0;    // workgroups of the attention on the chip at once
     char info[192] = "";
 };
 
@@ -55,7 +56,8 @@ struct DqAttendArgs {
     float* scores_out;
     float decay;
 };
-size_t dq_attend_part_floats(const dq_kv_ctx* c);
+// the attention's workers and the size of their partial results
+int dq_attend_plan(dq_kv_ctx* c);
 int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s);
 
 namespace dq {

@@ -508,6 +508,8 @@ extern "C" int dq_kv_init(dq_kv_ctx** ctx, int batch, int q_heads, int kv_heads,
         DQ_FAIL(DQ_ERR_RANGE, "pages_per_seq * page_size exceeds 2^30 tokens");
     if ((__int128)pages * kv_heads * page_size > INT32_MAX)
         DQ_FAIL(DQ_ERR_RANGE, "pages * kv_heads * page_size exceeds 2^31 - 1 rows");
+    if (gather_scores && ((int64_t)pages_per_seq * page_size + 127) / 128 * 128 * (q_heads / kv_heads) > INT32_MAX / 4 - 64)
+        DQ_FAIL(DQ_ERR_RANGE, "pages_per_seq * page_size * (q_heads / kv_heads) scores exceed 2^31 bytes");
     dq_kv_ctx* c = new (std::nothrow) dq_kv_ctx();
     if (!c) DQ_FAIL(DQ_ERR_ALLOC, "host allocation for the cache context failed");
     (void)hipGetDevice(&c->device);
@@ -531,11 +533,14 @@ extern "C" int dq_kv_init(dq_kv_ctx** ctx, int batch, int q_heads, int kv_heads,
     // a head's moves: at most half its slots come free and as many fill them
     c->moves_stride = (size_t)c->cap / 2 + 1;
     const size_t moves = (size_t)batch * kv_heads * (1 + 2 * c->moves_stride);
-    c->part_floats = dq_attend_part_floats(c);
-    if (c->scores) c->s_stride = ((size_t)c->cap + 127) / 128 * 128;
+    if (int rc = dq_attend_plan(c)) {
+        dq_kv_release(c);
+        return rc;
+    }
+    if (c->scores) c->s_stride = ((size_t)c->cap + 127) / 128 * 128 * (q_heads / kv_heads);
     bool ok = hipMalloc(&c->bad, 8) == hipSuccess && hipMalloc(&c->moves, moves * 4) == hipSuccess &&
-              (!c->part_floats || hipMalloc(&c->part, c->part_floats * 4) == hipSuccess) &&
-              (!c->scores || hipMalloc(&c->s, (size_t)batch * q_heads * c->s_stride * 4) == hipSuccess);
+              hipMalloc(&c->part, c->part_floats * 4) == hipSuccess &&
+              (!c->scores || hipMalloc(&c->s, (size_t)batch * kv_heads * c->s_stride * 4) == hipSuccess);
     if (!ok) {
         dq_kv_release(c);
         DQ_FAIL(DQ_ERR_ALLOC, "device allocation for the cache context failed");

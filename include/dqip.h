@@ -691,8 +691,9 @@ void dq_rope_release(dq_rope_ctx* ctx);
  * cap <= 2^30, pages * kv_heads * page_size < 2^31; q_type (DQ_F32 / DQ_BF16 /
  * DQ_F16) of queries, new keys and values, and outputs; cache_type (DQ_BF16 /
  * DQ_F16 / DQ_I8), each with each. gather_scores != 0 lets dq_kv_attend gather
- * weights (batch * q_heads * cap fp32 more of workspace). Allocates every
- * device buffer of the context (none later). Errors: DQ_ERR_ARG, DQ_ERR_TYPE,
+ * weights (batch * q_heads * cap fp32 more of workspace; cap * q_heads /
+ * kv_heads below 2^29 - 192 then). Allocates every device buffer of the
+ * context (none later). Errors: DQ_ERR_ARG, DQ_ERR_TYPE,
  * DQ_ERR_RANGE, DQ_ERR_ALLOC, DQ_ERR_HIP.
  *
  * All calls are asynchronous on `stream` and allocate nothing. dq_kv_attend
