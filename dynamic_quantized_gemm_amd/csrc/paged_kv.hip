@@ -258,10 +258,18 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 // Of a head's n > budget tokens those with the `budget` largest keys stay,
 // where a key is the gathered weight as an ordered integer, the largest there
 // is for the first `sinks` and last `recent` tokens, ties going to the lowest
-// slot. One workgroup selects for one head: the budget-th largest key digit
-// by digit from histograms in LDS, then the slots below the budget that came
-// free and the slots beyond it that stay, in order, as two lists. A second
-// launch moves the rows, which are most of the traffic, with the whole chip.
+// slot. One workgroup of 16 waves selects for one head, each wave a run of
+// whole 64s of slots, so that ballots count in slot order:
+//   the keys, read once and kept in registers up to 32 a lane (beyond 32768
+//   tokens they are read again for every pass);
+//   the budget-th largest key, 8 bits at a time, from histograms in LDS, of
+//   which there are eight, by lane: weights of one magnitude would otherwise
+//   meet in one counter;
+//   the slots below the budget that came free and the slots beyond it that
+//   stay, in order, as two lists.
+// A second launch moves the rows, which are most of the traffic, with the whole
+// chip; where at most 64 rows of a head can move (a token at a time over the
+// budget) the first moves them itself.
 
 struct EvictArgs {
     const int32_t *lens, *newest;
@@ -277,6 +285,7 @@ struct EvictArgs {
     size_t moves_stride;
     int32_t* bad;
     int batch, Hk, cap, budget, sinks, recent, row_bytes;
+    int moves_too;  // the selection moves the rows itself
     KvGeom geom;
 };
 
@@ -288,98 +297,169 @@ __device__ __forceinline__ uint32_t evict_key(float score, int order, int sinks,
     return score != score ? 0xffffffffu : k;  // a NaN is the largest
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs A) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t wave_a[kSelWaves], wave_b[kSelWaves];
-    __shared__ uint32_t sh_prefix, sh_left;
-    const int item = blockIdx.x, b = item / A.Hk;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int n = A.lens[b];
-    if (n < 0 || n > A.cap) {
-        if (tid == 0 && item % A.Hk == 0) atomicAdd(A.bad, 1);
-        n = n < 0 ? 0 : A.cap;
+// one row of keys, values, scales, weight and number, by sixteen lanes
+__device__ __forceinline__ void move_row(const EvictArgs& A, int item, int b, int h, int dst, int src, int l) {
+    const int32_t* line = A.table + (size_t)b * A.geom.per_seq;
+    const size_t base = (size_t)item * A.cap;
+    if (l == 0) {
+        A.scores_out[base + dst] = A.scores[base + src];
+        A.order_out[base + dst] = A.order[base + src];
     }
+    const int32_t to = kv_row(line, (uint32_t)dst, h, A.geom), from = kv_row(line, (uint32_t)src, h, A.geom);
+    if (to < 0 || from < 0) {
+        if (l == 0) atomicAdd(A.bad, 1);
+        return;
+    }
+    const size_t to_b = (size_t)to * A.row_bytes, from_b = (size_t)from * A.row_bytes;
+    for (int o = l * 16; o < A.row_bytes; o += 256) {
+        const v4i x = *(const v4i*)((const char*)A.kc + from_b + o);
+        const v4i y = *(const v4i*)((const char*)A.vc + from_b + o);
+        *(v4i*)((char*)A.kc + to_b + o) = x;
+        *(v4i*)((char*)A.vc + to_b + o) = y;
+    }
+    if (A.ks && l == 0) {
+        A.ks[to] = A.ks[from];
+        A.vs[to] = A.vs[from];
+    }
+}
+
+constexpr int kHistCopies = 8;
+
+struct SelectShared {
+    uint32_t hist[256 * kHistCopies];
+    uint32_t a[kSelWaves], b[kSelWaves];
+    uint32_t digit, left, count;
+};
+
+// KPT: keys a lane holds in registers (0: they are read again every time)
+template <int KPT>
+__device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& sh, int item, int b, int n) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const size_t base = (size_t)item * A.cap;
     const float* sc = A.scores + base;
     const int32_t* od = A.order + base;
-    float* sco = A.scores_out + base;
-    int32_t* odo = A.order_out + base;
-    int32_t* count = A.moves + item;
-    if (n <= A.budget) {
-        for (int i = tid; i < n; i += kSelThreads) {
-            sco[i] = sc[i];
-            odo[i] = od[i];
-        }
-        if (tid == 0) *count = 0;
-        return;
-    }
     const long long recent_from = (long long)A.newest[b] - A.recent;
-    uint32_t prefix = 0, left = (uint32_t)A.budget;  // keys still to be found below the prefix's ties
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kSelThreads) {
-            const uint32_t k = evict_key(sc[i], od[i], A.sinks, recent_from);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    const int iters = (n + kSelThreads - 1) / kSelThreads;
+    const int i0 = wave * iters * 64 + lane;
+    constexpr int KR = KPT ? KPT : 1;
+    uint32_t reg[KR];
+    if constexpr (KPT != 0) {
+        float f[KR];
+        int32_t o[KR];
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            const int i = i0 + k * 64;
+            if (k < iters && i < n) {
+                f[k] = sc[i];
+                o[k] = od[i];
+            }
         }
-        __syncthreads();
-        if (tid == 0) {
-            uint32_t seen = 0;
-            int d = 255;
-            while (d > 0 && seen + hist[d] < left) seen += hist[d--];
-            sh_prefix = prefix | ((uint32_t)d << shift);
-            sh_left = left - seen;
-        }
-        __syncthreads();
-        prefix = sh_prefix;
-        left = sh_left;
+#pragma unroll
+        for (int k = 0; k < KPT; ++k)
+            reg[k] = k < iters && i0 + k * 64 < n ? evict_key(f[k], o[k], A.sinks, recent_from) : 0;
     }
-    // kept: key > prefix, or key == prefix among the first `left` such slots.
-    // A wave takes a run of whole 64s, so that ballots count in slot order.
-    const int run = (n + kSelWaves * 64 - 1) / (kSelWaves * 64) * 64;
-    const int i0 = wave * run, i1 = min(n, i0 + run);
+    auto key = [&](int k) -> uint32_t {
+        if constexpr (KPT != 0) return reg[k];
+        const int i = i0 + k * 64;
+        return i < n ? evict_key(sc[i], od[i], A.sinks, recent_from) : 0;
+    };
+    // f(k): the lane's k-th slot, i0 + 64 k
+    auto each = [&](auto f) {
+        if constexpr (KPT != 0) {
+#pragma unroll
+            for (int k = 0; k < KPT; ++k)
+                if (k < iters) f(k);
+        } else {
+            for (int k = 0; k < iters; ++k) f(k);
+        }
+    };
+    uint32_t prefix = 0, left = (uint32_t)A.budget;  // of the keys that tie with the prefix, so many stay
+    uint32_t* mine = sh.hist + (lane & (kHistCopies - 1));
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256 * kHistCopies; i += kSelThreads) sh.hist[i] = 0;
+        __syncthreads();
+        each([&](int k) {
+            const uint32_t x = key(k);
+            const bool in = i0 + k * 64 < n && (shift == 24 || (x >> (shift + 8)) == (prefix >> (shift + 8)));
+            if (in) atomicAdd(mine + ((x >> shift) & 255u) * kHistCopies, 1u);
+        });
+        __syncthreads();
+        if (tid < 64) {
+            // four digits a lane, from 255 down; the digit at which the count
+            // of larger ones would pass `left`
+            uint32_t c[4], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const u4* h = (const u4*)&sh.hist[(255 - (4 * lane + j)) * kHistCopies];
+                const u4 x = h[0], y = h[1];
+                c[j] = x[0] + x[1] + x[2] + x[3] + y[0] + y[1] + y[2] + y[3];
+                sum += c[j];
+            }
+            uint32_t before = sum;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const uint32_t z = __shfl_up(before, o);
+                if (lane >= o) before += z;
+            }
+            before -= sum;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before < left && before + c[j] >= left) {
+                    sh.digit = 255 - (4 * lane + j);
+                    sh.left = left - before;
+                }
+                before += c[j];
+            }
+        }
+        __syncthreads();
+        prefix |= sh.digit << shift;
+        left = sh.left;
+    }
+    // kept: key > prefix, or key == prefix among the first `left` such slots
     const unsigned long long below = (1ull << lane) - 1;
     uint32_t ties = 0;
-    for (int i = i0 + lane; i - lane < i1; i += 64) {
-        const bool tie = i < i1 && evict_key(sc[i], od[i], A.sinks, recent_from) == prefix;
-        ties += __popcll(__ballot(tie));
-    }
-    if (lane == 0) wave_a[wave] = ties;
+    each([&](int k) { ties += __popcll(__ballot(i0 + k * 64 < n && key(k) == prefix)); });
+    if (lane == 0) sh.a[wave] = ties;
     __syncthreads();
     uint32_t tie0 = 0;
-    for (int w = 0; w < wave; ++w) tie0 += wave_a[w];
+    for (int w = 0; w < wave; ++w) tie0 += sh.a[w];
     __syncthreads();
-    uint32_t holes = 0, movers = 0, t = tie0;
-    for (int i = i0 + lane; i - lane < i1; i += 64) {
-        const uint32_t k = i < i1 ? evict_key(sc[i], od[i], A.sinks, recent_from) : 0;
-        const unsigned long long eq = __ballot(i < i1 && k == prefix);
-        const bool kept = i < i1 && (k > prefix || (k == prefix && t + __popcll(eq & below) < left));
-        t += __popcll(eq);
-        holes += __popcll(__ballot(i < i1 && i < A.budget && !kept));
-        movers += __popcll(__ballot(kept && i >= A.budget));
-    }
+    // f(slot, hole, mover) for every slot in order
+    auto sort_out = [&](auto f) {
+        uint32_t t = tie0;
+        each([&](int k) {
+            const int i = i0 + k * 64;
+            const uint32_t x = key(k);
+            const unsigned long long eq = __ballot(i < n && x == prefix);
+            const bool kept = i < n && (x > prefix || (x == prefix && t + __popcll(eq & below) < left));
+            t += __popcll(eq);
+            f(i, kept, i < n && i < A.budget && !kept, kept && i >= A.budget);
+        });
+    };
+    uint32_t holes = 0, movers = 0;
+    sort_out([&](int, bool, bool hole, bool mover) {
+        holes += __popcll(__ballot(hole));
+        movers += __popcll(__ballot(mover));
+    });
     if (lane == 0) {
-        wave_a[wave] = holes;
-        wave_b[wave] = movers;
+        sh.a[wave] = holes;
+        sh.b[wave] = movers;
     }
     __syncthreads();
     uint32_t hole0 = 0, mover0 = 0, total = 0;
     for (int w = 0; w < kSelWaves; ++w) {
         if (w < wave) {
-            hole0 += wave_a[w];
-            mover0 += wave_b[w];
+            hole0 += sh.a[w];
+            mover0 += sh.b[w];
         }
-        total += wave_a[w];
+        total += sh.a[w];
     }
+    if (tid == 0) sh.count = total;
     int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
     int32_t* src = dst + A.moves_stride;
-    t = tie0;
-    for (int i = i0 + lane; i - lane < i1; i += 64) {
-        const uint32_t k = i < i1 ? evict_key(sc[i], od[i], A.sinks, recent_from) : 0;
-        const unsigned long long eq = __ballot(i < i1 && k == prefix);
-        const bool kept = i < i1 && (k > prefix || (k == prefix && t + __popcll(eq & below) < left));
-        t += __popcll(eq);
-        const bool hole = i < i1 && i < A.budget && !kept, mover = kept && i >= A.budget;
+    float* sco = A.scores_out + base;
+    int32_t* odo = A.order_out + base;
+    sort_out([&](int i, bool kept, bool hole, bool mover) {
         const unsigned long long hb = __ballot(hole), mb = __ballot(mover);
         if (hole) dst[hole0 + __popcll(hb & below)] = i;
         if (mover) src[mover0 + __popcll(mb & below)] = i;
@@ -387,17 +467,41 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs
         mover0 += __popcll(mb);
         if (kept && i < A.budget && sco != sc) sco[i] = sc[i];
         if (kept && i < A.budget && odo != od) odo[i] = od[i];
-    }
-    if (tid == 0) *count = (int32_t)total;
-    __syncthreads();
-    for (uint32_t m = tid; m < total; m += kSelThreads) {
-        sco[dst[m]] = sc[src[m]];
-        odo[dst[m]] = od[src[m]];
-    }
+    });
 }
 
-// rows of keys and values from src to dst slots: sixteen lanes a row, sixteen
-// rows of both a workgroup
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs A) {
+    __shared__ SelectShared sh;
+    const int item = blockIdx.x, b = item / A.Hk, h = item - b * A.Hk, tid = threadIdx.x;
+    int n = A.lens[b];
+    if (n < 0 || n > A.cap) {
+        if (tid == 0 && h == 0) atomicAdd(A.bad, 1);
+        n = n < 0 ? 0 : A.cap;
+    }
+    if (A.moves_too && h == 0 && tid == 0) A.lens_out[b] = min(n, A.budget);
+    if (n <= A.budget) {
+        const size_t base = (size_t)item * A.cap;
+        for (int i = tid; i < n; i += kSelThreads) {
+            A.scores_out[base + i] = A.scores[base + i];
+            A.order_out[base + i] = A.order[base + i];
+        }
+        if (tid == 0) A.moves[item] = 0;
+        return;
+    }
+    if (n <= KPT * kSelThreads) evict_select<KPT>(A, sh, item, b, n);
+    else if constexpr (KPT == 32) evict_select<0>(A, sh, item, b, n);
+    __syncthreads();
+    if (!A.moves_too) {
+        if (tid == 0) A.moves[item] = (int32_t)sh.count;
+        return;
+    }
+    const int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
+    const int32_t* src = dst + A.moves_stride;
+    for (uint32_t m = tid >> 4; m < sh.count; m += kSelThreads / 16) move_row(A, item, b, h, dst[m], src[m], tid & 15);
+}
+
+// sixteen rows of both keys and values a workgroup
 __global__ void __launch_bounds__(256) k_kv_evict_move(const EvictArgs A) {
     const int item = blockIdx.y, b = item / A.Hk, h = item - b * A.Hk;
     const int count = A.moves[item];
@@ -405,28 +509,10 @@ __global__ void __launch_bounds__(256) k_kv_evict_move(const EvictArgs A) {
         const int n = A.lens[b];
         A.lens_out[b] = n < 0 ? 0 : min(min(n, A.cap), A.budget);
     }
-    const int l = threadIdx.x & 15;
     const int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
     const int32_t* src = dst + A.moves_stride;
-    const int32_t* line = A.table + (size_t)b * A.geom.per_seq;
-    for (int m = blockIdx.x * 16 + (threadIdx.x >> 4); m < count; m += gridDim.x * 16) {
-        const int32_t to = kv_row(line, (uint32_t)dst[m], h, A.geom), from = kv_row(line, (uint32_t)src[m], h, A.geom);
-        if (to < 0 || from < 0) {
-            if (l == 0) atomicAdd(A.bad, 1);
-            continue;
-        }
-        const size_t to_b = (size_t)to * A.row_bytes, from_b = (size_t)from * A.row_bytes;
-        for (int o = l * 16; o < A.row_bytes; o += 256) {
-            const v4i x = *(const v4i*)((const char*)A.kc + from_b + o);
-            const v4i y = *(const v4i*)((const char*)A.vc + from_b + o);
-            *(v4i*)((char*)A.kc + to_b + o) = x;
-            *(v4i*)((char*)A.vc + to_b + o) = y;
-        }
-        if (A.ks && l == 0) {
-            A.ks[to] = A.ks[from];
-            A.vs[to] = A.vs[from];
-        }
-    }
+    for (int m = blockIdx.x * 16 + (threadIdx.x >> 4); m < count; m += gridDim.x * 16)
+        move_row(A, item, b, h, dst[m], src[m], threadIdx.x & 15);
 }
 
 __global__ void k_kv_take_bad(int32_t* bad, int32_t* out) { *out = atomicExch(bad, 0); }
@@ -738,13 +824,22 @@ extern "C" int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, in
     A.geom = ctx->geom;
     const hipStream_t s = (hipStream_t)stream;
     const int items = batch * ctx->Hk;
-    hipLaunchKernelGGL(k_kv_evict_select, dim3((unsigned)items), dim3(kSelThreads), 0, s, A);
+    // the most rows of a head that can move. A workgroup moves 64 by itself in
+    // less than a second launch takes; lens_out is then written while other
+    // heads still read lens, so not where they are one tensor
+    const int most = std::max(0, std::min(budget, ctx->cap - budget));
+    A.moves_too = most <= 64 && lens_out != lens;
+    const dim3 grid((unsigned)items), block(kSelThreads);
+    if (ctx->cap <= 2 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<2>), grid, block, 0, s, A);
+    else if (ctx->cap <= 8 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<8>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((k_kv_evict_select<32>), grid, block, 0, s, A);
     DQ_LAUNCH_CHECK("eviction's selection");
-    // workgroups for the most rows that can move, at most 2^14 in all
-    const int most = std::max(1, std::min(budget, ctx->cap - budget));
-    const int gx = std::max(1, std::min((most + 15) / 16, (1 << 14) / items));
-    hipLaunchKernelGGL(k_kv_evict_move, dim3((unsigned)gx, (unsigned)items), dim3(256), 0, s, A);
-    DQ_LAUNCH_CHECK("eviction's moves");
+    if (!A.moves_too) {
+        // workgroups for the most rows that can move, at most 2^14 in all
+        const int gx = std::max(1, std::min((most + 15) / 16, (1 << 14) / items));
+        hipLaunchKernelGGL(k_kv_evict_move, dim3((unsigned)gx, (unsigned)items), dim3(256), 0, s, A);
+        DQ_LAUNCH_CHECK("eviction's moves");
+    }
     return DQ_OK;
 }
 
