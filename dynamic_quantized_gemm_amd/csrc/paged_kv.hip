@@ -328,60 +328,56 @@ constexpr int kHistCopies = 8;
 struct SelectShared {
     uint32_t hist[256 * kHistCopies];
     uint32_t a[kSelWaves], b[kSelWaves];
-    uint32_t digit, left, count;
+    uint32_t digit, left, ties, count;
 };
 
-// KPT: keys a lane holds in registers (0: they are read again every time)
-template <int KPT>
+// KPT (up to 32): keys a lane holds at a time. MEM: there are more than that,
+// and every pass reads them again, KPT at a time.
+template <int KPT, bool MEM>
 __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& sh, int item, int b, int n) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const size_t base = (size_t)item * A.cap;
     const float* sc = A.scores + base;
     const int32_t* od = A.order + base;
     const long long recent_from = (long long)A.newest[b] - A.recent;
+    // slot k of a lane: i0 + 64 k; a wave's slots are one run
     const int iters = (n + kSelThreads - 1) / kSelThreads;
     const int i0 = wave * iters * 64 + lane;
-    constexpr int KR = KPT ? KPT : 1;
-    uint32_t reg[KR];
-    if constexpr (KPT != 0) {
-        float f[KR];
-        int32_t o[KR];
+    uint32_t x[KPT];
+    auto load = [&](int k0) {
+        float f[KPT];
+        int32_t o[KPT];
 #pragma unroll
         for (int k = 0; k < KPT; ++k) {
-            const int i = i0 + k * 64;
-            if (k < iters && i < n) {
-                f[k] = sc[i];
-                o[k] = od[i];
-            }
+            const int i = i0 + (k0 + k) * 64;
+            const bool in = k0 + k < iters && i < n;
+            f[k] = in ? sc[i] : 0.0f;
+            o[k] = in ? od[i] : 0;
         }
 #pragma unroll
-        for (int k = 0; k < KPT; ++k)
-            reg[k] = k < iters && i0 + k * 64 < n ? evict_key(f[k], o[k], A.sinks, recent_from) : 0;
-    }
-    auto key = [&](int k) -> uint32_t {
-        if constexpr (KPT != 0) return reg[k];
-        const int i = i0 + k * 64;
-        return i < n ? evict_key(sc[i], od[i], A.sinks, recent_from) : 0;
+        for (int k = 0; k < KPT; ++k) x[k] = evict_key(f[k], o[k], A.sinks, recent_from);
     };
-    // f(k): the lane's k-th slot, i0 + 64 k
-    auto each = [&](auto f) {
-        if constexpr (KPT != 0) {
-#pragma unroll
-            for (int k = 0; k < KPT; ++k)
-                if (k < iters) f(k);
-        } else {
-            for (int k = 0; k < iters; ++k) f(k);
+    // f(k0, valid): the keys x of slots k0 .., of which the bits of valid exist
+    auto blocks = [&](auto f) {
+        for (int k0 = 0; k0 < (MEM ? iters : 1); k0 += KPT) {
+            if (MEM) load(k0);
+            // slots of this lane in the block: i0 + 64 (k0 + k) < n, k0 + k < iters
+            const int have = max(0, min(iters, (n - i0 + 63) >> 6) - k0);
+            f(k0, have >= 32 ? 0xffffffffu : (1u << have) - 1);
         }
     };
+    if (!MEM) load(0);
     uint32_t prefix = 0, left = (uint32_t)A.budget;  // of the keys that tie with the prefix, so many stay
     uint32_t* mine = sh.hist + (lane & (kHistCopies - 1));
     for (int shift = 24; shift >= 0; shift -= 8) {
         for (int i = tid; i < 256 * kHistCopies; i += kSelThreads) sh.hist[i] = 0;
         __syncthreads();
-        each([&](int k) {
-            const uint32_t x = key(k);
-            const bool in = i0 + k * 64 < n && (shift == 24 || (x >> (shift + 8)) == (prefix >> (shift + 8)));
-            if (in) atomicAdd(mine + ((x >> shift) & 255u) * kHistCopies, 1u);
+        blocks([&](int, uint32_t valid) {
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) {
+                const bool in = (valid >> k & 1) && (shift == 24 || ((x[k] ^ prefix) >> (shift + 8)) == 0);
+                if (in) atomicAdd(mine + ((x[k] >> shift) & 255u) * kHistCopies, 1u);
+            }
         });
         __syncthreads();
         if (tid < 64) {
@@ -391,8 +387,8 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const u4* h = (const u4*)&sh.hist[(255 - (4 * lane + j)) * kHistCopies];
-                const u4 x = h[0], y = h[1];
-                c[j] = x[0] + x[1] + x[2] + x[3] + y[0] + y[1] + y[2] + y[3];
+                const u4 p = h[0], q = h[1];
+                c[j] = p[0] + p[1] + p[2] + p[3] + q[0] + q[1] + q[2] + q[3];
                 sum += c[j];
             }
             uint32_t before = sum;
@@ -407,6 +403,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
                 if (before < left && before + c[j] >= left) {
                     sh.digit = 255 - (4 * lane + j);
                     sh.left = left - before;
+                    sh.ties = c[j];
                 }
                 before += c[j];
             }
@@ -415,32 +412,55 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
         prefix |= sh.digit << shift;
         left = sh.left;
     }
-    // kept: key > prefix, or key == prefix among the first `left` such slots
+    // Which stay: key > prefix, or key == prefix among the first `left` such
+    // slots. Mostly all of those stay, and no order has to be found.
+    const bool all_ties = sh.ties == left;
     const unsigned long long below = (1ull << lane) - 1;
-    uint32_t ties = 0;
-    each([&](int k) { ties += __popcll(__ballot(i0 + k * 64 < n && key(k) == prefix)); });
-    if (lane == 0) sh.a[wave] = ties;
-    __syncthreads();
-    uint32_t tie0 = 0;
-    for (int w = 0; w < wave; ++w) tie0 += sh.a[w];
-    __syncthreads();
-    // f(slot, hole, mover) for every slot in order
+    uint32_t tie = 0;
+    if (!all_ties) {
+        blocks([&](int, uint32_t valid) {
+#pragma unroll
+            for (int k = 0; k < KPT; ++k) tie += __popcll(__ballot((valid >> k & 1) && x[k] == prefix));
+        });
+        if (lane == 0) sh.a[wave] = tie;
+        __syncthreads();
+        tie = 0;
+        for (int w = 0; w < wave; ++w) tie += sh.a[w];
+        __syncthreads();
+    }
+    // f(k0, kept, under): bits of the block's slots that stay, and of those
+    // below the budget
     auto sort_out = [&](auto f) {
-        uint32_t t = tie0;
-        each([&](int k) {
-            const int i = i0 + k * 64;
-            const uint32_t x = key(k);
-            const unsigned long long eq = __ballot(i < n && x == prefix);
-            const bool kept = i < n && (x > prefix || (x == prefix && t + __popcll(eq & below) < left));
-            t += __popcll(eq);
-            f(i, kept, i < n && i < A.budget && !kept, kept && i >= A.budget);
+        uint32_t t = tie;
+        blocks([&](int k0, uint32_t valid) {
+            uint32_t kept = 0;
+            if (all_ties) {
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) kept |= (x[k] >= prefix ? 1u : 0u) << k;
+            } else {
+#pragma unroll
+                for (int k = 0; k < KPT; ++k) {
+                    const unsigned long long eq = __ballot((valid >> k & 1) && x[k] == prefix);
+                    const bool stays = x[k] > prefix || (x[k] == prefix && t + __popcll(eq & below) < left);
+                    kept |= (stays ? 1u : 0u) << k;
+                    t += __popcll(eq);
+                }
+            }
+            const int low = max(0, ((A.budget - i0 + 63) >> 6) - k0);
+            const uint32_t under = low >= 32 ? 0xffffffffu : (1u << low) - 1;
+            f(k0, kept & valid, under & valid);
         });
     };
     uint32_t holes = 0, movers = 0;
-    sort_out([&](int, bool, bool hole, bool mover) {
-        holes += __popcll(__ballot(hole));
-        movers += __popcll(__ballot(mover));
+    sort_out([&](int, uint32_t kept, uint32_t under) {
+        holes += __popc(under & ~kept);
+        movers += __popc(kept & ~under);
     });
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        holes += __shfl_xor(holes, o);
+        movers += __shfl_xor(movers, o);
+    }
     if (lane == 0) {
         sh.a[wave] = holes;
         sh.b[wave] = movers;
@@ -459,14 +479,26 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     int32_t* src = dst + A.moves_stride;
     float* sco = A.scores_out + base;
     int32_t* odo = A.order_out + base;
-    sort_out([&](int i, bool kept, bool hole, bool mover) {
-        const unsigned long long hb = __ballot(hole), mb = __ballot(mover);
-        if (hole) dst[hole0 + __popcll(hb & below)] = i;
-        if (mover) src[mover0 + __popcll(mb & below)] = i;
-        hole0 += __popcll(hb);
-        mover0 += __popcll(mb);
-        if (kept && i < A.budget && sco != sc) sco[i] = sc[i];
-        if (kept && i < A.budget && odo != od) odo[i] = od[i];
+    sort_out([&](int k0, uint32_t kept, uint32_t under) {
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+            // a 64 of slots lies below the budget, beyond it, or once astride
+            const int i = i0 + (k0 + k) * 64;
+            const bool hole = (under & ~kept) >> k & 1, mover = (kept & ~under) >> k & 1;
+            const unsigned long long hb = __ballot(hole), mb = __ballot(mover);
+            if (hb) {
+                if (hole) dst[hole0 + __popcll(hb & below)] = i;
+                hole0 += __popcll(hb);
+            }
+            if (mb) {
+                if (mover) src[mover0 + __popcll(mb & below)] = i;
+                mover0 += __popcll(mb);
+            }
+            if ((kept & under) >> k & 1) {
+                if (sco != sc) sco[i] = sc[i];
+                if (odo != od) odo[i] = od[i];
+            }
+        }
     });
 }
 
@@ -489,8 +521,8 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs
         if (tid == 0) A.moves[item] = 0;
         return;
     }
-    if (n <= KPT * kSelThreads) evict_select<KPT>(A, sh, item, b, n);
-    else if constexpr (KPT == 32) evict_select<0>(A, sh, item, b, n);
+    if (n <= KPT * kSelThreads) evict_select<KPT, false>(A, sh, item, b, n);
+    else if constexpr (KPT == 32) evict_select<KPT, true>(A, sh, item, b, n);
     __syncthreads();
     if (!A.moves_too) {
         if (tid == 0) A.moves[item] = (int32_t)sh.count;
