@@ -94,6 +94,39 @@ __device__ __forceinline__ void store_vec(S* p, const float (&f)[N]) {
 template <typename S>
 __device__ __forceinline__ void store_vec(S* p, const float (&f)[1]) { *p = (S)f[0]; }
 
+// VP pairs of a row: VP elements from lo and from hi, or 2 VP neighbours from lo.
+template <typename S, int VP, bool IL>
+__device__ __forceinline__ void load_pairs(const S* row, int lo, int hi, float (&a)[VP], float (&b)[VP]) {
+    if constexpr (IL) {
+        float e[2 * VP];
+        load_vec(row + lo, e);
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            a[i] = e[2 * i];
+            b[i] = e[2 * i + 1];
+        }
+    } else {
+        load_vec(row + lo, a);
+        load_vec(row + hi, b);
+    }
+}
+
+template <typename S, int VP, bool IL>
+__device__ __forceinline__ void store_pairs(S* row, int lo, int hi, const float (&a)[VP], const float (&b)[VP]) {
+    if constexpr (IL) {
+        float e[2 * VP];
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            e[2 * i] = a[i];
+            e[2 * i + 1] = b[i];
+        }
+        store_vec(row + lo, e);
+    } else {
+        store_vec(row + lo, a);
+        store_vec(row + hi, b);
+    }
+}
+
 // Element i of a tensor whose type is known at run time.
 __device__ __forceinline__ float load_any(const void* p, int type, long long i) {
     if (type == DQ_F32) return ((const float*)p)[i];

@@ -53,38 +53,6 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDppRowMirror, 0xF, 0xF, false));
 }
 
-template <typename S, int VP, bool IL>
-__device__ __forceinline__ void load_pairs(const S* row, int lo, int hi, float (&a)[VP], float (&b)[VP]) {
-    if constexpr (IL) {
-        float e[2 * VP];
-        load_vec(row + lo, e);
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            a[i] = e[2 * i];
-            b[i] = e[2 * i + 1];
-        }
-    } else {
-        load_vec(row + lo, a);
-        load_vec(row + hi, b);
-    }
-}
-
-template <typename S, int VP, bool IL>
-__device__ __forceinline__ void store_pairs(S* row, int lo, int hi, const float (&a)[VP], const float (&b)[VP]) {
-    if constexpr (IL) {
-        float e[2 * VP];
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            e[2 * i] = a[i];
-            e[2 * i + 1] = b[i];
-        }
-        store_vec(row + lo, e);
-    } else {
-        store_vec(row + lo, a);
-        store_vec(row + hi, b);
-    }
-}
-
 constexpr int kKvDimMax = 256;  // 128 pairs: eight a lane
 
 template <int TI, int TC, int VP, bool IL>
@@ -259,7 +227,7 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 // where a key is the gathered weight as an ordered integer, the largest there
 // is for the first `sinks` and last `recent` tokens, ties going to the lowest
 // slot. One workgroup of 16 waves selects for one head, each wave a run of
-// whole 64s of slots, so that ballots count in slot order:
+// slots, so that ballots count in slot order:
 //   the keys, read once and kept in registers up to 32 a lane (beyond 32768
 //   tokens they are read again for every pass);
 //   the budget-th largest key, 8 bits at a time, from histograms in LDS, of
@@ -331,8 +299,9 @@ struct SelectShared {
     uint32_t digit, left, ties, count;
 };
 
-// KPT (up to 32): keys a lane holds at a time. MEM: there are more than that,
-// and every pass reads them again, KPT at a time.
+// KPT (a multiple of 4, up to 32): keys a lane holds at a time, runs of four
+// neighbouring slots. MEM: there are more than that, and every pass reads them
+// again, KPT at a time.
 template <int KPT, bool MEM>
 __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& sh, int item, int b, int n) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -340,30 +309,57 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     const float* sc = A.scores + base;
     const int32_t* od = A.order + base;
     const long long recent_from = (long long)A.newest[b] - A.recent;
-    // slot k of a lane: i0 + 64 k; a wave's slots are one run
-    const int iters = (n + kSelThreads - 1) / kSelThreads;
-    const int i0 = wave * iters * 64 + lane;
-    uint32_t x[KPT];
-    auto load = [&](int k0) {
-        float f[KPT];
-        int32_t o[KPT];
+    // run k of a lane: slots i0 + 256 k + (0 .. 3); a wave's slots are one run
+    constexpr int KV = KPT / 4;
+    const int iters = (n + 4 * kSelThreads - 1) / (4 * kSelThreads);
+    const int i0 = wave * iters * 256 + lane * 4;
+    // f(k, weights, numbers, how many there are) for the lane's runs k0 + k, up
+    // to four of each on their way at a time
+    typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+    typedef int i4u __attribute__((ext_vector_type(4), aligned(4)));
+    constexpr int KG = KV < 4 ? KV : 4;
+    auto runs = [&](int k0, auto fn) {
 #pragma unroll
-        for (int k = 0; k < KPT; ++k) {
-            const int i = i0 + (k0 + k) * 64;
-            const bool in = k0 + k < iters && i < n;
-            f[k] = in ? sc[i] : 0.0f;
-            o[k] = in ? od[i] : 0;
+        for (int g = 0; g < KV; g += KG) {
+            f4u f[KG];
+            i4u o[KG];
+#pragma unroll
+            for (int k = 0; k < KG; ++k) {
+                const int i = i0 + (k0 + g + k) * 256;
+                f[k] = f4u{0, 0, 0, 0};
+                o[k] = i4u{0, 0, 0, 0};
+                if (k0 + g + k < iters && i + 4 <= n) {
+                    f[k] = *(const f4u*)(sc + i);
+                    o[k] = *(const i4u*)(od + i);
+                } else if (k0 + g + k < iters) {
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (i + j < n) {
+                            f[k][j] = sc[i + j];
+                            o[k][j] = od[i + j];
+                        }
+                }
+            }
+            issue_fence();
+#pragma unroll
+            for (int k = 0; k < KG; ++k)
+                fn(g + k, f[k], o[k], k0 + g + k < iters ? max(0, min(4, n - (i0 + (k0 + g + k) * 256))) : 0);
         }
-#pragma unroll
-        for (int k = 0; k < KPT; ++k) x[k] = evict_key(f[k], o[k], A.sinks, recent_from);
     };
-    // f(k0, valid): the keys x of slots k0 .., of which the bits of valid exist
+    uint32_t x[KPT];
+    // 0 is below every key: what stands in past a wave's or the head's end is
+    // never reached, since n > budget keys are above it
+    auto load = [&](int k0) {
+        runs(k0, [&](int k, f4u f, i4u o, int have) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * k + j] = j < have ? evict_key(f[j], o[j], A.sinks, recent_from) : 0;
+        });
+    };
+    // f(k0): the keys x of the lane's runs k0 ..
     auto blocks = [&](auto f) {
-        for (int k0 = 0; k0 < (MEM ? iters : 1); k0 += KPT) {
+        for (int k0 = 0; k0 < (MEM ? iters : 1); k0 += KV) {
             if (MEM) load(k0);
-            // slots of this lane in the block: i0 + 64 (k0 + k) < n, k0 + k < iters
-            const int have = max(0, min(iters, (n - i0 + 63) >> 6) - k0);
-            f(k0, have >= 32 ? 0xffffffffu : (1u << have) - 1);
+            f(k0);
         }
     };
     if (!MEM) load(0);
@@ -372,12 +368,11 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     for (int shift = 24; shift >= 0; shift -= 8) {
         for (int i = tid; i < 256 * kHistCopies; i += kSelThreads) sh.hist[i] = 0;
         __syncthreads();
-        blocks([&](int, uint32_t valid) {
+        blocks([&](int) {
 #pragma unroll
-            for (int k = 0; k < KPT; ++k) {
-                const bool in = (valid >> k & 1) && (shift == 24 || ((x[k] ^ prefix) >> (shift + 8)) == 0);
-                if (in) atomicAdd(mine + ((x[k] >> shift) & 255u) * kHistCopies, 1u);
-            }
+            for (int k = 0; k < KPT; ++k)
+                if (shift == 24 || ((x[k] ^ prefix) >> (shift + 8)) == 0)
+                    atomicAdd(mine + ((x[k] >> shift) & 255u) * kHistCopies, 1u);
         });
         __syncthreads();
         if (tid < 64) {
@@ -411,6 +406,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
         __syncthreads();
         prefix |= sh.digit << shift;
         left = sh.left;
+        if (sh.ties == left) break;  // all of the prefix stay, whatever follows it
     }
     // Which stay: key > prefix, or key == prefix among the first `left` such
     // slots. Mostly all of those stay, and no order has to be found.
@@ -418,9 +414,9 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     const unsigned long long below = (1ull << lane) - 1;
     uint32_t tie = 0;
     if (!all_ties) {
-        blocks([&](int, uint32_t valid) {
+        blocks([&](int) {
 #pragma unroll
-            for (int k = 0; k < KPT; ++k) tie += __popcll(__ballot((valid >> k & 1) && x[k] == prefix));
+            for (int k = 0; k < KPT; ++k) tie += __popcll(__ballot(x[k] == prefix));
         });
         if (lane == 0) sh.a[wave] = tie;
         __syncthreads();
@@ -432,23 +428,30 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     // below the budget
     auto sort_out = [&](auto f) {
         uint32_t t = tie;
-        blocks([&](int k0, uint32_t valid) {
-            uint32_t kept = 0;
-            if (all_ties) {
+        blocks([&](int k0) {
+            uint32_t kept = 0, under = 0;
 #pragma unroll
-                for (int k = 0; k < KPT; ++k) kept |= (x[k] >= prefix ? 1u : 0u) << k;
-            } else {
+            for (int k = 0; k < KV; ++k) {
+                const int low = k0 + k < iters ? max(0, min(4, A.budget - (i0 + (k0 + k) * 256))) : 0;
+                under |= ((1u << low) - 1) << (4 * k);
+                uint32_t before = 0;
+                if (!all_ties) {
 #pragma unroll
-                for (int k = 0; k < KPT; ++k) {
-                    const unsigned long long eq = __ballot((valid >> k & 1) && x[k] == prefix);
-                    const bool stays = x[k] > prefix || (x[k] == prefix && t + __popcll(eq & below) < left);
-                    kept |= (stays ? 1u : 0u) << k;
-                    t += __popcll(eq);
+                    for (int j = 0; j < 4; ++j) before += __popcll(__ballot(x[4 * k + j] == prefix) & below);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t y = x[4 * k + j];
+                    const bool stays = all_ties ? y >= prefix : y > prefix || (y == prefix && t + before < left);
+                    kept |= (stays ? 1u : 0u) << (4 * k + j);
+                    before += y == prefix;
+                }
+                if (!all_ties) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) t += __popcll(__ballot(x[4 * k + j] == prefix));
                 }
             }
-            const int low = max(0, ((A.budget - i0 + 63) >> 6) - k0);
-            const uint32_t under = low >= 32 ? 0xffffffffu : (1u << low) - 1;
-            f(k0, kept & valid, under & valid);
+            f(k0, kept, under);
         });
     };
     uint32_t holes = 0, movers = 0;
@@ -479,25 +482,38 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     int32_t* src = dst + A.moves_stride;
     float* sco = A.scores_out + base;
     int32_t* odo = A.order_out + base;
-    sort_out([&](int k0, uint32_t kept, uint32_t under) {
+    const bool copies = sco != sc || odo != od;
+    // the slots i + j of bits j, behind those of lower lanes and earlier runs
+    auto list = [&](int32_t* to, uint32_t& at, uint32_t bits, int i) {
+        if (!__ballot(bits)) return;
+        uint32_t before = at;
 #pragma unroll
-        for (int k = 0; k < KPT; ++k) {
-            // a 64 of slots lies below the budget, beyond it, or once astride
-            const int i = i0 + (k0 + k) * 64;
-            const bool hole = (under & ~kept) >> k & 1, mover = (kept & ~under) >> k & 1;
-            const unsigned long long hb = __ballot(hole), mb = __ballot(mover);
-            if (hb) {
-                if (hole) dst[hole0 + __popcll(hb & below)] = i;
-                hole0 += __popcll(hb);
-            }
-            if (mb) {
-                if (mover) src[mover0 + __popcll(mb & below)] = i;
-                mover0 += __popcll(mb);
-            }
-            if ((kept & under) >> k & 1) {
-                if (sco != sc) sco[i] = sc[i];
-                if (odo != od) odo[i] = od[i];
-            }
+        for (int j = 0; j < 4; ++j) {
+            const unsigned long long m = __ballot(bits >> j & 1);
+            before += __popcll(m & below);
+            at += __popcll(m);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (bits >> j & 1) to[before++] = i + j;
+    };
+    sort_out([&](int k0, uint32_t kept, uint32_t under) {
+        // weights and numbers of the slots that stay where they are
+        if (copies && __ballot(kept & under))
+            runs(k0, [&](int k, f4u f, i4u o, int) {
+                const int i = i0 + (k0 + k) * 256;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if ((kept & under) >> (4 * k + j) & 1) {
+                        sco[i + j] = f[j];
+                        odo[i + j] = o[j];
+                    }
+            });
+#pragma unroll
+        for (int k = 0; k < KV; ++k) {
+            const int i = i0 + (k0 + k) * 256;
+            list(dst, hole0, (under & ~kept) >> (4 * k) & 15u, i);
+            list(src, mover0, (kept & ~under) >> (4 * k) & 15u, i);
         }
     });
 }
@@ -862,7 +878,7 @@ extern "C" int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, in
     const int most = std::max(0, std::min(budget, ctx->cap - budget));
     A.moves_too = most <= 64 && lens_out != lens;
     const dim3 grid((unsigned)items), block(kSelThreads);
-    if (ctx->cap <= 2 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<2>), grid, block, 0, s, A);
+    if (ctx->cap <= 4 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<4>), grid, block, 0, s, A);
     else if (ctx->cap <= 8 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<8>), grid, block, 0, s, A);
     else hipLaunchKernelGGL((k_kv_evict_select<32>), grid, block, 0, s, A);
     DQ_LAUNCH_CHECK("eviction's selection");

@@ -31,9 +31,10 @@ struct RopeArgs {
     long long xt, xh, yt, yh;
     uint32_t threads;  // tokens * chunks * lanes
     int tokens, heads, D, R, inverse;
-    int chunk;         // heads a thread walks
     KvDiv lanes, chunks;
 };
+
+constexpr int kRopeHeads = 4;  // heads of a thread that are on their way at a time
 
 template <int TYPE, int VP, bool IL>
 __global__ void __launch_bounds__(256) k_rope(const RopeArgs A) {
@@ -43,9 +44,22 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs A) {
     const uint32_t rest = kv_div(id, A.lanes);
     const int i0 = (int)(id - rest * A.lanes.d) * VP;
     const uint32_t t = kv_div(rest, A.chunks);
-    const int h0 = (int)(rest - t * A.chunks.d) * A.chunk;
-    const int h1 = min(A.heads, h0 + A.chunk);
+    // heads h0, h0 + step, ..: neighbouring threads take neighbouring heads
+    const int h0 = (int)(rest - t * A.chunks.d), step = (int)A.chunks.d;
     const bool turn = i0 < A.R / 2;
+    int lo, hi;
+    kv_pair(i0, A.D, A.R, IL, &lo, &hi);
+    const S* x = (const S*)A.x + t * A.xt;
+    S* y = (S*)A.y + t * A.yt;
+    // the first heads are on their way while the angles are computed
+    float a[kRopeHeads][VP], b[kRopeHeads][VP];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int k = 0; k < kRopeHeads; ++k)
+            load_pairs<S, VP, IL>(x + (h + k * step < A.heads ? h + k * step : h0) * A.xh, lo, hi, a[k], b[k]);
+    };
+    load(h0);
+    issue_fence();
     float c[VP], s[VP];
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
@@ -54,46 +68,19 @@ __global__ void __launch_bounds__(256) k_rope(const RopeArgs A) {
         if (turn) rope_cos_sin(A.pos[(size_t)A.axis[i0 + i] * A.tokens + t], A.freq[i0 + i], &c[i], &s[i]);
         if (A.inverse) s[i] = -s[i];
     }
-    int lo, hi;
-    kv_pair(i0, A.D, A.R, IL, &lo, &hi);
-    const S* x = (const S*)A.x + t * A.xt;
-    S* y = (S*)A.y + t * A.yt;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-        const S* xr = x + h * A.xh;
-        S* yr = y + h * A.yh;
-        float a[VP], b[VP];
-        if (IL) {
-            float e[2 * VP];
-            load_vec(xr + lo, e);
+    for (int h = h0; h < A.heads; h += kRopeHeads * step) {
+        if (h != h0) load(h);
 #pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                a[i] = e[2 * i];
-                b[i] = e[2 * i + 1];
-            }
-        } else {
-            load_vec(xr + lo, a);
-            load_vec(xr + hi, b);
-        }
-        if (turn) {
+        for (int k = 0; k < kRopeHeads; ++k) {
+            if (turn) {
 #pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                const float u = a[i] * c[i] - b[i] * s[i];
-                b[i] = b[i] * c[i] + a[i] * s[i];
-                a[i] = u;
+                for (int i = 0; i < VP; ++i) {
+                    const float u = a[k][i] * c[i] - b[k][i] * s[i];
+                    b[k][i] = b[k][i] * c[i] + a[k][i] * s[i];
+                    a[k][i] = u;
+                }
             }
-        }
-        if (IL) {
-            float e[2 * VP];
-#pragma unroll
-            for (int i = 0; i < VP; ++i) {
-                e[2 * i] = a[i];
-                e[2 * i + 1] = b[i];
-            }
-            store_vec(yr + lo, e);
-        } else {
-            store_vec(yr + lo, a);
-            store_vec(yr + hi, b);
+            if (h + k * step < A.heads) store_pairs<S, VP, IL>(y + (h + k * step) * A.yh, lo, hi, a[k], b[k]);
         }
     }
 }
@@ -233,7 +220,6 @@ extern "C" int dq_rope_forward(const dq_rope_ctx* ctx, const void* x, dq_dtype t
     if (tokens * chunks > INT32_MAX || tokens * chunks * lanes > (int64_t)UINT32_MAX - 256)
         DQ_FAIL(DQ_ERR_RANGE, "too many tokens for one launch");
     A.tokens = (int)tokens;
-    A.chunk = chunk;
     A.lanes = make_kvdiv((uint32_t)lanes);
     A.chunks = make_kvdiv((uint32_t)chunks);
     A.threads = (uint32_t)(tokens * chunks * lanes);
