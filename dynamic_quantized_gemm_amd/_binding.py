@@ -197,16 +197,23 @@ def _ptr(t, what="tensor", nbytes=0):
 _DQIP_DIMS = {}
 
 
+_raw_stream = _get_device = None
+
+
 def _current_stream():
     """Handle of torch's current stream on the current device. The raw
-    accessor skips building a Stream object (about 2.5 us a call); the
-    public call is the fallback where torch lacks it."""
-    import torch
+    accessors skip building a Stream object (about 2.5 us a call) and are
+    looked up once; the public call is the fallback where torch lacks them."""
+    global _raw_stream, _get_device
+    if _raw_stream is None:
+        import torch
 
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_device()  # the raw accessors need torch's device state
+    return _raw_stream(_get_device())
 
 
 def _stream(stream):
@@ -809,15 +816,28 @@ def dq_lstm_release(ctx):
 
 # -------------------------------------- rotary positions, paged cache
 
+def _dev(t, what, nbytes):
+    """_ptr for calls that take many small tensors: what passes the checks
+    passes them in a third of the time, the rest is _ptr's to name."""
+    if t is None:
+        return None
+    try:
+        if t.is_cuda and t.nbytes >= nbytes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, what, nbytes)
+
+
 def _rows(t, what, heads, dim, elem, tokens=None):
     """(pointer, token stride, head stride) of a [tokens, heads, dim] device
     tensor whose rows of dim are dense; tokens and heads may be strided."""
-    if t.device.type != "cuda":
-        raise DQError(DQ_ERR_ARG, what, "not a device tensor")
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (tokens is not None and shape[0] != tokens):
         raise DQError(DQ_ERR_ARG, what, f"[{'tokens' if tokens is None else tokens}, {heads}, {dim}] expected, "
                                         f"got {list(shape)}")
+    if not t.is_cuda:
+        raise DQError(DQ_ERR_ARG, what, "not a device tensor")
     ts, hs, ds = t.stride()
     if ds != 1 and dim > 1:
         raise DQError(DQ_ERR_ARG, what, "the last dimension must be dense")
@@ -864,7 +884,7 @@ def dq_rope_forward(ctx, x, positions, y, inverse=False, type_=None, stream=None
     elem = _ELEM.get(type_, 0)
     xp, xt, xh = _rows(x, w, heads, dim, elem)
     yp, yt, yh = _rows(y, w, heads, dim, elem, n)
-    _check(load().dq_rope_forward(ctx, xp, type_, n, heads, xt, xh, _ptr(positions, w, 4 * axes * n), yp, yt, yh,
+    _check(load().dq_rope_forward(ctx, xp, type_, n, heads, xt, xh, _dev(positions, w, 4 * axes * n), yp, yt, yh,
                                   1 if inverse else 0, _stream(stream)), w)
 
 
@@ -906,8 +926,8 @@ def _kv_dims(ctx, what):
 
 
 def _kv_cache(d, what, seqs, block_table, k_cache, v_cache, k_scale, v_scale):
-    return (_ptr(block_table, what, 4 * seqs * d[4]), _ptr(k_cache, what, d[7]), _ptr(v_cache, what, d[7]),
-            _ptr(k_scale, what, d[8]), _ptr(v_scale, what, d[8]))
+    return (_dev(block_table, what, 4 * seqs * d[4]), _dev(k_cache, what, d[7]), _dev(v_cache, what, d[7]),
+            _dev(k_scale, what, d[8]), _dev(v_scale, what, d[8]))
 
 
 def dq_kv_append(ctx, k, v, index, block_table, k_cache, v_cache, k_scale=None, v_scale=None, seq_ids=None, q=None,
@@ -924,14 +944,14 @@ def dq_kv_append(ctx, k, v, index, block_table, k_cache, v_cache, k_scale=None, 
     qp, qt, qh, op, pp = None, 0, 0, None, None
     if q is not None:
         qp, qt, qh = _rows(q, w, d[1], d[3], d[6], n)
-        op = _ptr(q_out, w, n * d[1] * d[3] * d[6])
+        op = _dev(q_out, w, n * d[1] * d[3] * d[6])
     if rope is not None:
         if rope not in _ROPE_DIMS:
             raise DQError(DQ_ERR_STATE, w, "no rotary context")
-        pp = _ptr(positions, w, 4 * _ROPE_DIMS[rope][1] * n)
+        pp = _dev(positions, w, 4 * _ROPE_DIMS[rope][1] * n)
     elif positions is not None:
         raise DQError(DQ_ERR_ARG, w, "rope and positions go together")
-    _check(load().dq_kv_append(ctx, n, kp, kt, kh, vp, vt, vh, _ptr(index, w, 4 * n), _ptr(seq_ids, w, 4 * n),
+    _check(load().dq_kv_append(ctx, n, kp, kt, kh, vp, vt, vh, _dev(index, w, 4 * n), _dev(seq_ids, w, 4 * n),
                                *_kv_cache(d, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
                                qp, qt, qh, op, rope, pp, _stream(stream)), w)
 
@@ -944,9 +964,9 @@ def dq_kv_read(ctx, index, block_table, k_cache, v_cache, k_scale=None, v_scale=
     d = _kv_dims(ctx, w)
     n = int(index.numel())
     size = n * d[2] * d[3] * d[6]
-    _check(load().dq_kv_read(ctx, n, _ptr(index, w, 4 * n), _ptr(seq_ids, w, 4 * n),
+    _check(load().dq_kv_read(ctx, n, _dev(index, w, 4 * n), _dev(seq_ids, w, 4 * n),
                              *_kv_cache(d, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
-                             _ptr(k_out, w, size), _ptr(v_out, w, size), _stream(stream)), w)
+                             _dev(k_out, w, size), _dev(v_out, w, size), _stream(stream)), w)
 
 
 def dq_kv_attend(ctx, q, lens, block_table, k_cache, v_cache, k_scale, v_scale, out, sm_scale, lse=None, window=0,
@@ -959,10 +979,10 @@ def dq_kv_attend(ctx, q, lens, block_table, k_cache, v_cache, k_scale, v_scale, 
     n = int(q.shape[0])
     qp, qt, qh = _rows(q, w, d[1], d[3], d[6])
     size = 4 * n * d[2] * d[5]
-    _check(load().dq_kv_attend(ctx, n, qp, qt, qh, _ptr(lens, w, 4 * n),
+    _check(load().dq_kv_attend(ctx, n, qp, qt, qh, _dev(lens, w, 4 * n),
                                *_kv_cache(d, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
-                               _ptr(out, w, n * d[1] * d[3] * d[6]), sm_scale, _ptr(lse, w, 4 * n * d[1]), window,
-                               _ptr(scores, w, size), _ptr(scores_out, w, size), decay, _stream(stream)), w)
+                               _dev(out, w, n * d[1] * d[3] * d[6]), sm_scale, _dev(lse, w, 4 * n * d[1]), window,
+                               _dev(scores, w, size), _dev(scores_out, w, size), decay, _stream(stream)), w)
 
 
 def dq_kv_evict(ctx, budget, lens, newest, scores, order, block_table, k_cache, v_cache, k_scale, v_scale,
@@ -973,10 +993,10 @@ def dq_kv_evict(ctx, budget, lens, newest, scores, order, block_table, k_cache, 
     d = _kv_dims(ctx, w)
     n = int(lens.numel())
     size = 4 * n * d[2] * d[5]
-    _check(load().dq_kv_evict(ctx, n, int(budget), int(recent), int(sinks), _ptr(lens, w, 4 * n),
-                              _ptr(newest, w, 4 * n), _ptr(scores, w, size), _ptr(order, w, size),
+    _check(load().dq_kv_evict(ctx, n, int(budget), int(recent), int(sinks), _dev(lens, w, 4 * n),
+                              _dev(newest, w, 4 * n), _dev(scores, w, size), _dev(order, w, size),
                               *_kv_cache(d, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
-                              _ptr(scores_out, w, size), _ptr(order_out, w, size), _ptr(lens_out, w, 4 * n),
+                              _dev(scores_out, w, size), _dev(order_out, w, size), _dev(lens_out, w, 4 * n),
                               _stream(stream)), w)
 
 

@@ -102,6 +102,7 @@ class _Fake:
             dense.append(n)
         self._s, self._dense = tuple(stride or dense), tuple(dense)
         self.device = type("D", (), {"type": device})()
+        self.is_cuda = device == "cuda"
         self.dtype = "torch.bfloat16"
 
     def stride(self):
@@ -115,6 +116,10 @@ class _Fake:
 
     def element_size(self):
         return self._e
+
+    @property
+    def nbytes(self):
+        return self.numel() * self._e
 
     def is_contiguous(self):
         return self._s == self._dense
