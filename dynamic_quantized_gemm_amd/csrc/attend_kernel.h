@@ -52,6 +52,8 @@ struct AttendArgs {
     size_t s_stride;  // (s_stride apart), runs of 32 tokens: [G][32]
     float* l2;    // [batch * Hq] log2 of the sum of exp
     float* part;  // [workers][2][16][D + 4]: maximum, sum, -, -, weighted values
+    int2* parts;  // [batch * Hk * tiles]: the first of the workers that share an
+                  // item's units and their number, 0 where the item needs no join
     int32_t* bad;
     KvGeom geom;
 };
@@ -63,27 +65,26 @@ __device__ __forceinline__ int attend_len(const AttendArgs& A, int b, bool* bad)
     return *bad ? 0 : n;
 }
 
-__device__ __forceinline__ int64_t attend_units(const AttendArgs& A, int b) {
-    bool bad;
-    return (int64_t)kv_units(attend_len(A, b, &bad), A.a.window) * (A.Hk * A.tiles);
-}
-
 struct AttendScan {
     int64_t sum[4];  // of each wave
     int64_t base;
-    int b;
+    int b, len;
 };
 
 // All units of the batch, by a workgroup of 256 threads that take runs of
-// sequences; *mine is the number of units before this thread's run, *run its
-// length.
-__device__ __forceinline__ int64_t attend_scan(const AttendArgs& A, AttendScan* sh, int64_t* mine, int* run) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    *run = (A.a.batch + 255) / 256;
+// sequences. The thread whose run has the first unit of worker w leaves that
+// unit's sequence, its length and the number of units before it in *sh (the
+// caller's barrier makes them seen).
+__device__ __forceinline__ KvShare attend_scan(const AttendArgs& A, AttendScan* sh, int w) {
+    const int tid = threadIdx.x, lane = tid & 63, run = (A.a.batch + 255) / 256;
+    const int items = A.Hk * A.tiles;
     int64_t x = 0;
-    for (int i = 0; i < *run; ++i) {
-        const int b = tid * *run + i;
-        if (b < A.a.batch) x += attend_units(A, b);
+    int len = 0;
+    for (int i = 0; i < run; ++i) {
+        const int b = tid * run + i;
+        bool bad;
+        len = b < A.a.batch ? attend_len(A, b, &bad) : 0;
+        x += (int64_t)kv_units(len, A.a.window) * items;
     }
     int64_t y = x;
     for (int o = 1; o < 64; o <<= 1) {
@@ -97,13 +98,24 @@ __device__ __forceinline__ int64_t attend_scan(const AttendArgs& A, AttendScan* 
         if (w < (tid >> 6)) y += sh->sum[w];
         total += sh->sum[w];
     }
-    *mine = y - x;
-    return total;
-}
-
-// Workers that have a unit: a part is joined from consecutive ones.
-__device__ __forceinline__ int attend_workers(const AttendArgs& A, int64_t units) {
-    return (int)min((int64_t)A.workers, units);
+    const KvShare share = kv_share(total, A.workers);
+    const int64_t u = w < share.workers ? kv_first(w, share) : -1;
+    int64_t base = y - x;
+    if (u >= base && u < y) {
+        int b = tid * run;
+        if (run > 1)
+            for (;; ++b) {
+                bool bad;
+                len = attend_len(A, b, &bad);
+                const int64_t n = (int64_t)kv_units(len, A.a.window) * items;
+                if (u < base + n) break;
+                base += n;
+            }
+        sh->b = b;
+        sh->len = len;
+        sh->base = base;
+    }
+    return share;
 }
 
 // The scores of a run of 32 tokens (from the window's first on) of a
@@ -205,52 +217,27 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
     const int items = A.Hk * A.tiles;
 
     // ---- this workgroup's units
-    int64_t mine;
-    int run;
-    const int64_t units = uniform(attend_scan(A, &scan, &mine, &run));
-    // sequences without a token
-    for (int b = blockIdx.x; b < A.a.batch; b += A.workers) {
-        bool bad;
-        if (attend_len(A, b, &bad) > 0) continue;
-        if (bad && tid == 0) atomicAdd(A.bad, 1);
-        const float o = bad ? __builtin_nanf("") : 0.0f, l2 = bad ? __builtin_nanf("") : -__builtin_inff();
-        for (int i = tid; i < A.Hq * D; i += 256) store_any(A.a.out, A.q_type, (long long)b * A.Hq * D + i, o);
-        for (int i = tid; i < A.Hq; i += 256) {
-            A.l2[(size_t)b * A.Hq + i] = l2;
-            if (A.a.lse) A.a.lse[(size_t)b * A.Hq + i] = l2;
-        }
-    }
-    const int workers = uniform(attend_workers(A, units));
-    if ((int)blockIdx.x >= workers) return;
-    int64_t u = kv_first(blockIdx.x, workers, units);
-    const int64_t u_end = kv_first(blockIdx.x + 1, workers, units);
-    {
-        int64_t x = mine;
-        for (int i = 0; i < run; ++i) {
-            const int b = tid * run + i;
-            if (b >= A.a.batch) break;
-            const int64_t nb = attend_units(A, b);
-            if (u >= x && u < x + nb) {
-                scan.b = b;
-                scan.base = x;
-            }
-            x += nb;
-        }
-    }
+    KvShare share = attend_scan(A, &scan, blockIdx.x);
+    share.units = uniform(share.units);
+    share.workers = uniform(share.workers);
+    share.each = uniform(share.each);
     __syncthreads();
-    int b = uniform(scan.b);
+    int b = uniform(scan.b), len = uniform(scan.len);
     int64_t base = uniform(scan.base);
+    const bool works = (int)blockIdx.x < share.workers;
+    int64_t u = works ? kv_first(blockIdx.x, share) : 0;
+    const int64_t u_end = works ? kv_first(blockIdx.x + 1, share) : 0;
 
     while (u < u_end) {
-        bool bad_len;
-        const int len = attend_len(A, b, &bad_len);
         const int first = kv_first_token(len, A.a.window), nb = kv_units(len, A.a.window);
         if (u >= base + (int64_t)nb * items) {
             base += (int64_t)nb * items;
-            ++b;
+            bool bad;
+            len = attend_len(A, ++b, &bad);
             continue;
         }
-        const int item = (int)((u - base) / nb);
+        const int64_t rel = u - base;
+        const int item = rel >> 32 ? (int)(rel / nb) : (int)((uint32_t)rel / (uint32_t)nb);
         const int64_t item_u = base + (int64_t)item * nb;
         const int unit0 = (int)(u - item_u);
         const int count = (int)(min(u_end, item_u + nb) - u);
@@ -336,7 +323,16 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
         // ---- queries as MFMA operands
         u4 q[C][NQ];
         float scale = A.a.sm_scale * kLog2e;
-        {
+        if (NQ == 1 && (CT != DQ_F16 || A.q_type == DQ_F16)) {
+            // as they are
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int d0 = CT == DQ_I8 ? (c >> 1) * 64 + g * 16 + (c & 1) * 8 : c * 32 + g * 8;
+                const bool in = n16 < heads && (FULL || d0 < D);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) q[c][0][w] = in ? raw[c][w] : 0;
+            }
+        } else {
             float x[C][8];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
@@ -348,14 +344,14 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
                     if (NQ == 3) {
                         y = __uint_as_float(raw[c][j % QW]);
                     } else {
+                        // fp16 on a bf16 or int8 cache, bf16 on an fp16 one
                         const uint16_t h = (uint16_t)(raw[c][j / 2] >> (16 * (j & 1)));
-                        const bool half = NQ == 2 || (CT == DQ_F16 && A.q_type == DQ_F16);
-                        y = half ? (float)__builtin_bit_cast(_Float16, h) : bf16_bits_to_f32(h);
+                        y = CT == DQ_F16 ? bf16_bits_to_f32(h) : (float)__builtin_bit_cast(_Float16, h);
                     }
                     x[c][j] = in ? y : 0.0f;
                 }
             }
-            if (CT == DQ_F16 && A.q_type != DQ_F16) {
+            if (CT == DQ_F16) {
                 // to [2^14, 2^15): the power of two of the row's largest
                 float top = 0.0f;
 #pragma unroll
@@ -528,6 +524,9 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
         }
         __syncthreads();
         const bool whole = unit0 == 0 && count == nb;
+        if (unit0 == 0 && tid == 0)
+            A.parts[(size_t)b * items + item] =
+                int2{(int)blockIdx.x, whole ? 0 : kv_worker(item_u + nb - 1, share) - (int)blockIdx.x + 1};
         float* part = A.part + (size_t)(2 * blockIdx.x + (unit0 == 0 ? 1 : 0)) * kHeadTile * (D + 4);
         for (int e = tid; e < heads * (D / 4); e += 256) {
             const int n = e / (D / 4), d = (e - n * (D / 4)) * 4;
@@ -564,6 +563,20 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
         }
         __syncthreads();
         u += count;
+    }
+
+    // ---- sequences without a token
+    for (int b = blockIdx.x; b < A.a.batch; b += A.workers) {
+        bool bad;
+        if (attend_len(A, b, &bad) > 0) continue;
+        if (bad && tid == 0) atomicAdd(A.bad, 1);
+        const float o = bad ? __builtin_nanf("") : 0.0f, l2 = bad ? __builtin_nanf("") : -__builtin_inff();
+        for (int i = tid; i < A.Hq * D; i += 256) store_any(A.a.out, A.q_type, (long long)b * A.Hq * D + i, o);
+        for (int i = tid; i < A.Hq; i += 256) {
+            A.l2[(size_t)b * A.Hq + i] = l2;
+            if (A.a.lse) A.a.lse[(size_t)b * A.Hq + i] = l2;
+        }
+        for (int i = tid; i < items; i += 256) A.parts[(size_t)b * items + i] = int2{0, 0};
     }
 }
 

@@ -75,18 +75,41 @@ DQ_HD void kv_pair(int i, int D, int R, bool interleaved, int* a, int* b) {
 //
 // The attention's tokens are cut into units of kKvUnit tokens of one sequence
 // and one head tile. Units are numbered sequence by sequence, head tile by
-// head tile; worker w of W takes units [kv_first(w), kv_first(w + 1)), so all
-// have the same number of units to within one, whatever the lengths.
+// head tile, and each worker takes a run of them, so all have the same number
+// to within one, whatever the lengths. Up to kKvRound units a worker, all runs
+// are of the same whole number (fewer workers then, none with more to do):
+// runs that begin in the middle of a sequence and end in the next one's cost
+// more than an idle worker.
 constexpr int kKvUnit = 128;
+constexpr int kKvRound = 8;
 
 DQ_HD int kv_first_token(int len, int window) { return window > 0 && len > window ? len - window : 0; }
 DQ_HD int kv_units(int len, int window) {
     return (len - kv_first_token(len, window) + kKvUnit - 1) / kKvUnit;
 }
-DQ_HD int64_t kv_first(int w, int W, int64_t units) { return units * w / W; }
-// The worker that takes unit u: the largest w with kv_first(w) <= u.
-DQ_HD int kv_worker(int64_t u, int W, int64_t units) {
-    return (int)(((u + 1) * W - 1) / units);
+
+struct KvShare {
+    int64_t units;
+    int workers;  // that have a unit
+    int each;     // units of a worker; 0: shares to within one
+};
+DQ_HD KvShare kv_share(int64_t units, int most) {
+    const int64_t each = (units + most - 1) / most;
+    KvShare s;
+    s.units = units;
+    s.each = each <= kKvRound ? (int)each : 0;
+    s.workers = each == 0 ? 0 : s.each ? (int)((units + each - 1) / each) : most;
+    return s;
+}
+// the first unit of worker w
+DQ_HD int64_t kv_first(int w, const KvShare& s) {
+    if (!s.each) return s.units * w / s.workers;
+    const int64_t u = (int64_t)w * s.each;
+    return u < s.units ? u : s.units;
+}
+// the worker that takes unit u: the largest w with kv_first(w) <= u
+DQ_HD int kv_worker(int64_t u, const KvShare& s) {
+    return s.each ? (int)(u / s.each) : (int)(((u + 1) * s.workers - 1) / s.units);
 }
 
 }  // namespace dq

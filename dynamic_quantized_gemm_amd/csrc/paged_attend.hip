@@ -31,30 +31,16 @@ struct FinishParts {
 };
 
 __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
-    __shared__ AttendScan scan;
     __shared__ float s_top[4], s_sum[4], s_l2[kFinishHeads], s_f[kMaxWorkers];
     __shared__ f4 s_acc[256];
     const int tid = threadIdx.x, lane = tid & 63;
     const int item = blockIdx.y, b = item / A.Hk, hk = item - b * A.Hk;
-    int64_t mine;
-    int run;
-    const int64_t units = attend_scan(A, &scan, &mine, &run);
-    if (tid == b / run) {
-        for (int i = tid * run; i < b; ++i) mine += attend_units(A, i);
-        scan.base = mine;
-    }
-    __syncthreads();
-    bool bad;
-    const int len = attend_len(A, b, &bad), first = kv_first_token(len, A.a.window), nb = kv_units(len, A.a.window);
-    if (nb == 0) return;
-    const int workers = attend_workers(A, units);
     auto parts_of = [&](int x) {
-        const int64_t u = scan.base + (int64_t)(hk * A.tiles + x / kHeadTile) * nb;
-        const int w0 = kv_worker(u, workers, units), w1 = kv_worker(u + nb - 1, workers, units);
+        const int2 w = A.parts[(size_t)item * A.tiles + x / kHeadTile];
         FinishParts p;
         p.stride = kHeadTile * (A.D + 4);
-        p.base = A.part + (size_t)2 * w0 * p.stride + (size_t)(x % kHeadTile) * (A.D + 4);
-        p.count = w0 == w1 ? 0 : w1 - w0 + 1;
+        p.base = A.part + (size_t)2 * w.x * p.stride + (size_t)(x % kHeadTile) * (A.D + 4);
+        p.count = w.y;
         return p;
     };
     // ---- outputs: the parts' factors once, in LDS, then groups of D / 4 lanes
@@ -107,6 +93,8 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
     }
     if (!A.s) return;
     // ---- gathered weights
+    bool bad;
+    const int len = attend_len(A, b, &bad), first = kv_first_token(len, A.a.window);
     const float* in = A.a.scores + (size_t)item * A.cap;
     float* out = A.a.scores_out + (size_t)item * A.cap;
     for (int t = blockIdx.x * 256 + tid; t < first; t += gridDim.x * 256) out[t] = in[t] * A.a.decay;
@@ -194,7 +182,8 @@ int dq_attend_plan(dq_kv_ctx* c) {
         per_cu < 1)
         DQ_FAIL(DQ_ERR_HIP, "the attention kernel does not fit the device");
     c->attend_workers = std::min(kMaxWorkers, c->cus * std::min(per_cu, 2));
-    c->part_floats = (size_t)c->attend_workers * 2 * kHeadTile * (c->D + 4) + (size_t)c->batch * c->Hq;
+    const size_t items = (size_t)c->batch * c->Hk * ((c->Hq / c->Hk + kHeadTile - 1) / kHeadTile);
+    c->part_floats = (size_t)c->attend_workers * 2 * kHeadTile * (c->D + 4) + 2 * items + (size_t)c->batch * c->Hq;
     return DQ_OK;
 }
 
@@ -211,7 +200,8 @@ int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s) {
     A.s = a.scores ? c->s : nullptr;
     A.s_stride = c->s_stride;
     A.part = c->part;
-    A.l2 = c->part + (size_t)c->attend_workers * 2 * kHeadTile * (c->D + 4);
+    A.parts = (int2*)(c->part + (size_t)c->attend_workers * 2 * kHeadTile * (c->D + 4));
+    A.l2 = (float*)(A.parts + (size_t)a.batch * A.Hk * A.tiles);
     A.bad = c->bad;
     A.geom = c->geom;
     const size_t es = kv_elem_bytes(c->q_type);

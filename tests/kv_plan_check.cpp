@@ -53,16 +53,20 @@ static void pairs(int D, int R, bool il) {
 }
 
 static void shares(int64_t units, int W) {
-    CHECK(kv_first(0, W, units) == 0 && kv_first(W, W, units) == units);
+    const KvShare s = kv_share(units, W);
+    CHECK(s.workers >= (units > 0) && s.workers <= W && s.workers <= units);
+    if (units == 0) return;
+    CHECK(kv_first(0, s) == 0 && kv_first(s.workers, s) == units);
     int64_t least = units, most = 0;
-    for (int w = 0; w < W; ++w) {
-        const int64_t a = kv_first(w, W, units), b = kv_first(w + 1, W, units);
-        CHECK(a <= b);
-        least = b - a < least ? b - a : least;
+    for (int w = 0; w < s.workers; ++w) {
+        const int64_t a = kv_first(w, s), b = kv_first(w + 1, s);
+        CHECK(a < b);  // every worker has something
+        if (w + 1 < s.workers) least = b - a < least ? b - a : least;
         most = b - a > most ? b - a : most;
-        for (int64_t u = a; u < b; ++u) CHECK(kv_worker(u, W, units) == w);
+        for (int64_t u = a; u < b; ++u) CHECK(kv_worker(u, s) == w);
     }
     CHECK(most - least <= 1);
+    CHECK(most <= (units + W - 1) / W);  // no worker has more than the evenest share
 }
 
 int main() {
@@ -79,7 +83,7 @@ int main() {
             pairs(D, R, true);
         }
     for (int W : {1, 2, 3, 255, 512, 768})
-        for (int64_t u : {1ll, 2ll, 7ll, 511ll, 512ll, 513ll, 4099ll, 38001ll}) shares(u, W);
+        for (int64_t u : {0ll, 1ll, 2ll, 7ll, 511ll, 512ll, 513ll, 4099ll, 38001ll}) shares(u, W);
     for (int n : {0, 1, 127, 128, 129, 5000})
         for (int w : {0, 1, 128, 1000, 6000}) {
             const int first = kv_first_token(n, w), units = kv_units(n, w);
