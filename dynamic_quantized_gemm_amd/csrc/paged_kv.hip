@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 //   tokens they are read again for every pass);
 //   the budget-th largest key, 8 bits at a time, from histograms in LDS, of
 //   which there are eight, by lane: weights of one magnitude would otherwise
-//   meet in one counter;
+//   meet in one counter. The keys with the first 8 bits are left in LDS on the
+//   way, and the third and fourth pass look at those alone (32768 tokens: 5 us
+//   less), unless they are more than 4096;
 //   the slots below the budget that came free and the slots beyond it that
 //   stay, in order, as two lists.
 // A second launch moves the rows, which are most of the traffic, with the whole
@@ -274,38 +276,58 @@ __device__ __forceinline__ uint32_t evict_key(float score, int order, int sinks,
     return score != score ? 0xffffffffu : k;  // a NaN is the largest
 }
 
-// one row of keys, values, scales, weight and number, by sixteen lanes
-__device__ __forceinline__ void move_row(const EvictArgs& A, int item, int b, int h, int dst, int src, int l) {
+// Up to R rows of keys, values, scales, weights and numbers by sixteen lanes:
+// lane j < R finds row j's place, then all rows are on their way before the
+// first is written. A key row and its value row are one run of pieces.
+constexpr int kMoveRows = 4;
+
+__device__ __forceinline__ void move_rows(const EvictArgs& A, int item, int b, int h, const int32_t* dst,
+                                          const int32_t* src, int count, int l) {
     const int32_t* line = A.table + (size_t)b * A.geom.per_seq;
     const size_t base = (size_t)item * A.cap;
-    if (l == 0) {
-        A.scores_out[base + dst] = A.scores[base + src];
-        A.order_out[base + dst] = A.order[base + src];
+    int32_t to = -1, from = -1;
+    if (l < min(count, kMoveRows)) {
+        const int d = dst[l], s = src[l];
+        to = kv_row(line, (uint32_t)d, h, A.geom);
+        from = kv_row(line, (uint32_t)s, h, A.geom);
+        A.scores_out[base + d] = A.scores[base + s];
+        A.order_out[base + d] = A.order[base + s];
+        if (to < 0 || from < 0) {
+            atomicAdd(A.bad, 1);
+            to = from = -1;
+        } else if (A.ks) {
+            A.ks[to] = A.ks[from];
+            A.vs[to] = A.vs[from];
+        }
     }
-    const int32_t to = kv_row(line, (uint32_t)dst, h, A.geom), from = kv_row(line, (uint32_t)src, h, A.geom);
-    if (to < 0 || from < 0) {
-        if (l == 0) atomicAdd(A.bad, 1);
-        return;
+    // (all sixteen lanes take part in the exchange; in the loop some may not)
+    int32_t t[kMoveRows], f[kMoveRows];
+#pragma unroll
+    for (int j = 0; j < kMoveRows; ++j) {
+        t[j] = __shfl(to, j, 16);
+        f[j] = __shfl(from, j, 16);
     }
-    const size_t to_b = (size_t)to * A.row_bytes, from_b = (size_t)from * A.row_bytes;
-    for (int o = l * 16; o < A.row_bytes; o += 256) {
-        const v4i x = *(const v4i*)((const char*)A.kc + from_b + o);
-        const v4i y = *(const v4i*)((const char*)A.vc + from_b + o);
-        *(v4i*)((char*)A.kc + to_b + o) = x;
-        *(v4i*)((char*)A.vc + to_b + o) = y;
-    }
-    if (A.ks && l == 0) {
-        A.ks[to] = A.ks[from];
-        A.vs[to] = A.vs[from];
+    const int pieces = A.row_bytes / 16;
+    for (int o = l; o < 2 * pieces; o += 16) {
+        char* c = (char*)(o < pieces ? A.kc : A.vc) + (o < pieces ? o : o - pieces) * 16;
+        v4i x[kMoveRows];
+#pragma unroll
+        for (int j = 0; j < kMoveRows; ++j)
+            if (f[j] >= 0) x[j] = __builtin_nontemporal_load((const v4i*)(c + (size_t)f[j] * A.row_bytes));
+#pragma unroll
+        for (int j = 0; j < kMoveRows; ++j)
+            if (t[j] >= 0) *(v4i*)(c + (size_t)t[j] * A.row_bytes) = x[j];
     }
 }
 
 constexpr int kHistCopies = 8;
+constexpr int kNear = 4096;  // keys that share the first 8 bits, kept in LDS
 
 struct SelectShared {
     uint32_t hist[256 * kHistCopies];
     uint32_t a[kSelWaves], b[kSelWaves];
-    uint32_t digit, left, ties, count;
+    uint32_t digit, left, ties, count, found;
+    uint32_t near[kNear];
 };
 
 // KPT (a multiple of 4, up to 32): keys a lane holds at a time, runs of four
@@ -374,15 +396,27 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     if (!MEM) load(0);
     uint32_t prefix = 0, left = (uint32_t)A.budget;  // of the keys that tie with the prefix, so many stay
     uint32_t* mine = sh.hist + (lane & (kHistCopies - 1));
+    bool listed = false;  // the keys with the prefix's first 8 bits are in LDS
+    uint32_t found = 0;   // so many
     for (int shift = 24; shift >= 0; shift -= 8) {
         for (int i = tid; i < 256 * kHistCopies; i += kSelThreads) sh.hist[i] = 0;
+        if (tid == 0) sh.found = 0;
         __syncthreads();
-        blocks([&](int) {
+        if (shift < 16 && listed) {
+            for (uint32_t i = tid; i < found; i += kSelThreads) {
+                const uint32_t y = sh.near[i];
+                if (((y ^ prefix) >> (shift + 8)) == 0) atomicAdd(mine + ((y >> shift) & 255u) * kHistCopies, 1u);
+            }
+        } else {
+            blocks([&](int) {
 #pragma unroll
-            for (int k = 0; k < KPT; ++k)
-                if (shift == 24 || ((x[k] ^ prefix) >> (shift + 8)) == 0)
-                    atomicAdd(mine + ((x[k] >> shift) & 255u) * kHistCopies, 1u);
-        });
+                for (int k = 0; k < KPT; ++k)
+                    if (shift == 24 || ((x[k] ^ prefix) >> (shift + 8)) == 0) {
+                        atomicAdd(mine + ((x[k] >> shift) & 255u) * kHistCopies, 1u);
+                        if (shift == 16 && listed) sh.near[atomicAdd(&sh.found, 1u)] = x[k];
+                    }
+            });
+        }
         __syncthreads();
         if (tid < 64) {
             // four digits a lane, from 255 down; the digit at which the count
@@ -416,6 +450,10 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
         prefix |= sh.digit << shift;
         left = sh.left;
         if (sh.ties == left) break;  // all of the prefix stay, whatever follows it
+        if (shift == 24) {
+            found = sh.ties;
+            listed = found <= kNear;
+        }
     }
     // Which stay: key > prefix, or key == prefix among the first `left` such
     // slots. Mostly all of those stay, and no order has to be found.
@@ -463,10 +501,12 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
             f(k0, kept, under);
         });
     };
-    uint32_t holes = 0, movers = 0;
+    uint32_t holes = 0, movers = 0, kept0 = 0, under0 = 0;
     sort_out([&](int, uint32_t kept, uint32_t under) {
         holes += __popc(under & ~kept);
         movers += __popc(kept & ~under);
+        kept0 = kept;
+        under0 = under;
     });
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
@@ -506,7 +546,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
         for (int j = 0; j < 4; ++j)
             if (bits >> j & 1) to[before++] = i + j;
     };
-    sort_out([&](int k0, uint32_t kept, uint32_t under) {
+    auto put = [&](int k0, uint32_t kept, uint32_t under) {
         // weights and numbers of the slots that stay where they are
         if (copies && __ballot(kept & under))
             runs(k0, [&](int k, f4u f, i4u o, int) {
@@ -524,7 +564,9 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
             list(dst, hole0, (under & ~kept) >> (4 * k) & 15u, i);
             list(src, mover0, (kept & ~under) >> (4 * k) & 15u, i);
         }
-    });
+    };
+    if (MEM) sort_out(put);
+    else put(0, kept0, under0);
 }
 
 template <int KPT>
@@ -555,10 +597,11 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs
     }
     const int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
     const int32_t* src = dst + A.moves_stride;
-    for (uint32_t m = tid >> 4; m < sh.count; m += kSelThreads / 16) move_row(A, item, b, h, dst[m], src[m], tid & 15);
+    for (int m = (tid >> 4) * kMoveRows; m < (int)sh.count; m += kSelThreads / 16 * kMoveRows)
+        move_rows(A, item, b, h, dst + m, src + m, (int)sh.count - m, tid & 15);
 }
 
-// sixteen rows of both keys and values a workgroup
+// 64 rows of both keys and values a workgroup. Bound by their traffic.
 __global__ void __launch_bounds__(256) k_kv_evict_move(const EvictArgs A) {
     const int item = blockIdx.y, b = item / A.Hk, h = item - b * A.Hk;
     const int count = A.moves[item];
@@ -568,8 +611,8 @@ __global__ void __launch_bounds__(256) k_kv_evict_move(const EvictArgs A) {
     }
     const int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
     const int32_t* src = dst + A.moves_stride;
-    for (int m = blockIdx.x * 16 + (threadIdx.x >> 4); m < count; m += gridDim.x * 16)
-        move_row(A, item, b, h, dst[m], src[m], threadIdx.x & 15);
+    for (int m = (blockIdx.x * 16 + (threadIdx.x >> 4)) * kMoveRows; m < count; m += gridDim.x * 16 * kMoveRows)
+        move_rows(A, item, b, h, dst + m, src + m, count - m, threadIdx.x & 15);
 }
 
 __global__ void k_kv_take_bad(int32_t* bad, int32_t* out) { *out = atomicExch(bad, 0); }
@@ -896,7 +939,7 @@ extern "C" int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, in
     DQ_LAUNCH_CHECK("eviction's selection");
     if (!A.moves_too) {
         // workgroups for the most rows that can move, at most 2^14 in all
-        const int gx = std::max(1, std::min((most + 15) / 16, (1 << 14) / items));
+        const int gx = std::max(1, std::min((most + 63) / 64, (1 << 14) / items));
         hipLaunchKernelGGL(k_kv_evict_move, dim3((unsigned)gx, (unsigned)items), dim3(256), 0, s, A);
         DQ_LAUNCH_CHECK("eviction's moves");
     }
