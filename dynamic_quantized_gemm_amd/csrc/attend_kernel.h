@@ -48,6 +48,7 @@ struct AttendArgs {
     int q_type, Hq, Hk, D, cap, G, tiles;  // tiles: head tiles of a key-value head
     int workers;
     int q_vec;  // queries can be loaded 16 bytes at a time
+    int whole;  // a workgroup takes whole items, and there is nothing to finish
     float* s;         // NULL: scores are not kept; else for each key-value head
     size_t s_stride;  // (s_stride apart), runs of 32 tokens: [G][32]
     float* l2;    // [batch * Hq] log2 of the sum of exp
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
     __shared__ AttendScan scan;
     __shared__ int32_t s_row[4][32];
     __shared__ float s_scale[4][64];
-    __shared__ float j_max[4][16], j_sum[4][16];
+    __shared__ float j_max[4][16], j_sum[4][16], j_l2[16];
     __shared__ float j_acc[4][16 * kAcc];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -217,30 +218,52 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
     const int items = A.Hk * A.tiles;
 
     // ---- this workgroup's units
-    KvShare share = attend_scan(A, &scan, blockIdx.x);
-    share.units = uniform(share.units);
-    share.workers = uniform(share.workers);
-    share.each = uniform(share.each);
-    __syncthreads();
-    int b = uniform(scan.b), len = uniform(scan.len);
-    int64_t base = uniform(scan.base);
-    const bool works = (int)blockIdx.x < share.workers;
-    int64_t u = works ? kv_first(blockIdx.x, share) : 0;
-    const int64_t u_end = works ? kv_first(blockIdx.x + 1, share) : 0;
+    // [u, u_end) are units, or items where a workgroup takes whole items
+    KvShare share{};
+    int b = 0, len = 0;
+    int64_t base = 0, u = blockIdx.x, u_end = (int64_t)A.a.batch * items;
+    if (!A.whole) {
+        share = attend_scan(A, &scan, blockIdx.x);
+        share.units = uniform(share.units);
+        share.workers = uniform(share.workers);
+        share.each = uniform(share.each);
+        __syncthreads();
+        b = uniform(scan.b);
+        len = uniform(scan.len);
+        base = uniform(scan.base);
+        const bool works = (int)blockIdx.x < share.workers;
+        u = works ? kv_first(blockIdx.x, share) : 0;
+        u_end = works ? kv_first(blockIdx.x + 1, share) : 0;
+    }
 
     while (u < u_end) {
+        if (A.whole) {
+            bool bad;
+            b = (int)((uint32_t)u / (uint32_t)items);
+            len = uniform(attend_len(A, b, &bad));
+        }
         const int first = kv_first_token(len, A.a.window), nb = kv_units(len, A.a.window);
-        if (u >= base + (int64_t)nb * items) {
+        if (A.whole ? nb == 0 : u >= base + (int64_t)nb * items) {
+            if (A.whole) {
+                u += A.workers;
+                continue;
+            }
             base += (int64_t)nb * items;
             bool bad;
             len = attend_len(A, ++b, &bad);
             continue;
         }
-        const int64_t rel = u - base;
-        const int item = rel >> 32 ? (int)(rel / nb) : (int)((uint32_t)rel / (uint32_t)nb);
-        const int64_t item_u = base + (int64_t)item * nb;
-        const int unit0 = (int)(u - item_u);
-        const int count = (int)(min(u_end, item_u + nb) - u);
+        int item, unit0 = 0, count = nb;
+        int64_t item_u = 0;
+        if (A.whole) {
+            item = (int)((uint32_t)u - (uint32_t)b * (uint32_t)items);
+        } else {
+            const int64_t rel = u - base;
+            item = rel >> 32 ? (int)(rel / nb) : (int)((uint32_t)rel / (uint32_t)nb);
+            item_u = base + (int64_t)item * nb;
+            unit0 = (int)(u - item_u);
+            count = (int)(min(u_end, item_u + nb) - u);
+        }
         const int hk = item / A.tiles, h0 = hk * A.G + (item - hk * A.tiles) * kHeadTile;
         const int heads = min(kHeadTile, (hk + 1) * A.G - h0);
         const int32_t* line = A.a.table + (size_t)b * A.geom.per_seq;
@@ -524,7 +547,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
         }
         __syncthreads();
         const bool whole = unit0 == 0 && count == nb;
-        if (unit0 == 0 && tid == 0)
+        if (unit0 == 0 && tid == 0 && !A.whole)
             A.parts[(size_t)b * items + item] =
                 int2{(int)blockIdx.x, whole ? 0 : kv_worker(item_u + nb - 1, share) - (int)blockIdx.x + 1};
         float* part = A.part + (size_t)(2 * blockIdx.x + (unit0 == 0 ? 1 : 0)) * kHeadTile * (D + 4);
@@ -545,12 +568,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 const size_t i = (size_t)b * A.Hq + h0 + n;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    store_any(A.a.out, A.q_type, (long long)(i * D + d + k), sum == 0.0f ? 0.0f : o[k] * inv);
+                if (sum == 0.0f) o = f4{0, 0, 0, 0};
+                store4_any(A.a.out, A.q_type, i * D + d, o * inv);
                 if (d == 0) {
                     const float l2 = sum == 0.0f ? -__builtin_inff() : ref + __builtin_amdgcn_logf(sum);
                     A.l2[i] = l2;
+                    // for the gathered weights: 2^(s - inf) = 0 where there is none
+                    j_l2[n] = sum == 0.0f ? __builtin_inff() : l2;
                     if (A.a.lse) A.a.lse[i] = l2 * kLn2;
                 }
             } else {
@@ -561,8 +585,23 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
                 }
             }
         }
+        if (A.whole && A.s) {
+            // ---- gathered weights; the scores that the waves kept are read
+            // back by others, once all of them have reached the L2 cache
+            wait_vmcnt<0>();
+            __syncthreads();
+            const size_t row = (size_t)(b * A.Hk + hk) * A.cap;
+            for (int t = tid; t < first; t += 256) A.a.scores_out[row + t] = A.a.scores[row + t] * A.a.decay;
+            const float* kept = A.s + attend_score_at(A, b * A.Hk + hk, 0);
+            for (int r = tid; r < len - first; r += 256) {
+                const float* y = kept + (size_t)(r >> 5) * (32 * A.G) + (r & 31);
+                float p = 0.0f;
+                for (int x = 0; x < heads; ++x) p += __builtin_amdgcn_exp2f(y[x * 32] - j_l2[x]);
+                A.a.scores_out[row + first + r] = A.a.scores[row + first + r] * A.a.decay + p;
+            }
+        }
         __syncthreads();
-        u += count;
+        u += A.whole ? A.workers : count;
     }
 
     // ---- sequences without a token
@@ -576,7 +615,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
             A.l2[(size_t)b * A.Hq + i] = l2;
             if (A.a.lse) A.a.lse[(size_t)b * A.Hq + i] = l2;
         }
-        for (int i = tid; i < items; i += 256) A.parts[(size_t)b * items + i] = int2{0, 0};
+        for (int i = tid; i < items && !A.whole; i += 256) A.parts[(size_t)b * items + i] = int2{0, 0};
     }
 }
 

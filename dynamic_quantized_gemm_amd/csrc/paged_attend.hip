@@ -84,9 +84,8 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
             for (int i = 0; i < groups; ++i) o += s_acc[i * lanes + d];
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const size_t at = (size_t)b * A.Hq + hk * A.G + x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                store_any(A.a.out, A.q_type, (long long)(at * A.D + 4 * d + k), sum == 0.0f ? 0.0f : o[k] * inv);
+            if (sum == 0.0f) o = f4{0, 0, 0, 0};
+            store4_any(A.a.out, A.q_type, at * A.D + 4 * d, o * inv);
             if (d == 0 && A.a.lse) A.a.lse[at] = (sum == 0.0f ? -__builtin_inff() : ref + __builtin_amdgcn_logf(sum)) * kLn2;
         }
         __syncthreads();
@@ -166,6 +165,9 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
     }
 }
 
+// Units of 128 tokens that a workgroup takes alone rather than share a head.
+constexpr int kWholeUnits = 4;
+
 AttendKernel pick_kernel(const dq_kv_ctx* c) {
     return c->cache_type == DQ_I8 ? attend_i8(c->q_type, c->D)
            : c->cache_type == DQ_F16 ? attend_f16(c->q_type, c->D) : attend_bf16(c->q_type, c->D);
@@ -208,13 +210,16 @@ int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s) {
     A.q_vec = (uintptr_t)a.q % 16 == 0 && a.q_ts * es % 16 == 0 && a.q_hs * es % 16 == 0;
     // as many workers as the most units that the call can have, up to the chip's
     const int64_t per_item = kv_units(c->cap, a.window);
-    const int64_t most = per_item * a.batch * A.Hk * A.tiles;
-    A.workers = (int)std::min<int64_t>(most, c->attend_workers);
+    const int64_t items = (int64_t)a.batch * A.Hk * A.tiles;
+    // Short sequences are not split: a workgroup takes whole items, finishes
+    // them itself and looks up no other sequence's length.
+    A.whole = per_item <= kWholeUnits && (!a.scores || A.tiles == 1);
+    A.workers = (int)std::min<int64_t>(A.whole ? items : per_item * items, c->attend_workers);
     hipLaunchKernelGGL(pick_kernel(c), dim3((unsigned)A.workers), dim3(256), 0, s, A);
     DQ_LAUNCH_CHECK("attention");
-    if (per_item > 1 || a.scores) {
+    if (!A.whole) {
         const int chunks = a.scores ? (c->cap + 1023) / 1024 : 0;
-        const int gx = std::max(std::min(A.G, per_item > 1 ? 16 : 1), std::min(chunks, std::max(1, 8192 / (a.batch * c->Hk))));
+        const int gx = std::max(std::min(A.G, 16), std::min(chunks, std::max(1, 8192 / (a.batch * c->Hk))));
         hipLaunchKernelGGL(k_attend_finish, dim3((unsigned)gx, (unsigned)(a.batch * c->Hk)), dim3(256), 0, s, A);
         DQ_LAUNCH_CHECK("finish of the attention");
     }

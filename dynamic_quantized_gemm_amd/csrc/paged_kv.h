@@ -142,6 +142,15 @@ __device__ __forceinline__ void store_any(void* p, int type, long long i, float 
     else ((_Float16*)p)[i] = (_Float16)f;
 }
 
+// Four neighbouring elements, aligned to their size.
+__device__ __forceinline__ void store4_any(void* p, int type, size_t i, f4 f) {
+    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+    if (type == DQ_F32) *(f4*)((float*)p + i) = f;
+    else if (type == DQ_BF16) *(b4*)((__bf16*)p + i) = __builtin_convertvector(f, b4);
+    else *(h4*)((_Float16*)p + i) = __builtin_convertvector(f, h4);
+}
+
 // cos and sin of pos * freq (freq in turns, hi + lo). The product is reduced
 // to a fraction of a turn in fp64 with its remainder kept, so a position of 31
 // bits loses nothing, and the Taylor series on [-pi/4, pi/4] (first term left
