@@ -18,9 +18,9 @@
 //                   tokens into one lane, which are the 8 that the same lane
 //                   has to supply as the operand P^T: the weights never leave
 //                   their registers.
-// A lane loads E = DP / 16 neighbouring values of V for its 8 tokens, and
-// the A operand for d = E n + i (i < E) is the i-th of each: the transposition
-// is within a lane, one byte permutation for two values. Nothing goes through
+// A lane loads E = DP / 16 values of V for its 8 tokens (neighbours; of 192,
+// eight and four), and the A operand for d = E n + i (i < E) is the i-th of
+// each: the transposition is within a lane, one byte permutation for two values. Nothing goes through
 // LDS but 32 row numbers and scales for each 32 tokens.
 //
 // Precision. Products are of 16-bit operands, summed in fp32. int8 codes are
@@ -160,6 +160,21 @@ __device__ __forceinline__ u2 codes_bf16x4(uint32_t w) {
     return r;
 }
 
+// N words that will not be needed again, as many as possible at a time
+template <int N>
+__device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
+    constexpr int M = N >= 4 ? 4 : N >= 2 ? 2 : 1;
+    typedef uint32_t V __attribute__((ext_vector_type(M), aligned(4)));
+    if constexpr (M == 1) {
+        w[0] = __builtin_nontemporal_load((const uint32_t*)p);
+    } else {
+        const V x = __builtin_nontemporal_load((const V*)p);
+#pragma unroll
+        for (int i = 0; i < M; ++i) w[i] = x[i];
+    }
+    if constexpr (N > M) load_words<N - M>(p + 4 * M, w + M);
+}
+
 template <int CT> struct AttendOps {  // bf16 products: bf16 and int8 caches
     static constexpr float kOffset = 0.0f;
     typedef __bf16 T;
@@ -195,14 +210,19 @@ __device__ __forceinline__ void pieces(const float (&x)[8], u4 (&out)[NP]) {
 }
 
 // CT: the cache's type; NQ, NP: pieces of queries and weights; DP: the head
-// size rounded up to 64, 128 or 256; FULL: it is that size.
+// size rounded up to 64, 128, 192 or 256; FULL: it is that size.
+// Two workgroups are on a compute unit where their registers fit.
+constexpr int attend_per_cu(int CT, int NQ, int DP) {
+    return DP == 256 ? (CT == DQ_I8 && NQ == 1 ? 2 : 1) : DP == 192 ? (NQ == 3 ? 1 : 2) : 2;
+}
 template <int CT, int NQ, int NP, int DP, bool FULL>
-__global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8 && NQ == 1) ? 3 : 2) k_attend(const AttendArgs A) {
+__global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const AttendArgs A) {
     typedef AttendOps<CT> Ops;
     typedef typename Ops::T T;
     constexpr int EB = CT == DQ_I8 ? 1 : 2;       // bytes of a value
     constexpr int E = DP / 16;                    // values of V a lane loads for a token
     constexpr int VW = E * EB / 4;                // their words
+    constexpr int EA = DP == 192 ? 8 : E;         // of them neighbours; of 192, four more lie past d = 128
     constexpr int C = DP / 32;                    // steps of 32 of q . k
     constexpr int KL = DP * EB / 64;              // 16-byte loads of K for 16 tokens
     constexpr int kAcc = DP + 4;
@@ -413,18 +433,12 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int32_t r = j < 4 ? ra[j] : rb[j - 4];
-                const int o = n16 * E * EB;
-                const char* p = (const char*)A.a.v + (size_t)(uint32_t)r * row_bytes + (FULL || o < row_bytes ? o : 0);
-                typedef uint32_t W __attribute__((ext_vector_type(VW < 4 ? VW : 4)));
-                if constexpr (VW == 1) {
-                    vf[j][0] = __builtin_nontemporal_load((const uint32_t*)p);
-                } else {
-#pragma unroll
-                    for (int w = 0; w < VW; w += 4) {
-                        const W x = __builtin_nontemporal_load((const W*)(p + 4 * w));
-#pragma unroll
-                        for (int i = 0; i < (VW < 4 ? VW : 4); ++i) vf[j][w + i] = x[i];
-                    }
+                const char* p = (const char*)A.a.v + (size_t)(uint32_t)r * row_bytes;
+                const int o = n16 * EA * EB;
+                load_words<EA * EB / 4>(p + (FULL || o < row_bytes ? o : 0), vf[j]);
+                if constexpr (DP == 192) {
+                    const int o2 = (128 + n16 * 4) * EB;
+                    load_words<EB>(p + (FULL || o2 < row_bytes ? o2 : 0), vf[j] + EA * EB / 4);
                 }
             }
             issue_fence();
@@ -542,7 +556,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : DP == 128 && (CT == DQ_I8
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int i = 0; i < E; i += 4)
-                    *(f4*)&j_acc[wave][n16 * kAcc + E * (4 * g + r) + i] =
+                    *(f4*)&j_acc[wave][n16 * kAcc + (i < EA ? EA * (4 * g + r) + i : 128 + 4 * (4 * g + r))] =
                         f4{acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]};
         }
         __syncthreads();
@@ -629,6 +643,7 @@ template <int CT, int NQ, int NP>
 AttendKernel attend_pick(int D) {
     if (D <= 64) return D == 64 ? k_attend<CT, NQ, NP, 64, true> : k_attend<CT, NQ, NP, 64, false>;
     if (D <= 128) return D == 128 ? k_attend<CT, NQ, NP, 128, true> : k_attend<CT, NQ, NP, 128, false>;
+    if (D <= 192) return D == 192 ? k_attend<CT, NQ, NP, 192, true> : k_attend<CT, NQ, NP, 192, false>;
     return D == 256 ? k_attend<CT, NQ, NP, 256, true> : k_attend<CT, NQ, NP, 256, false>;
 }
 

@@ -96,7 +96,11 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
     const int len = attend_len(A, b, &bad), first = kv_first_token(len, A.a.window);
     const float* in = A.a.scores + (size_t)item * A.cap;
     float* out = A.a.scores_out + (size_t)item * A.cap;
-    for (int t = blockIdx.x * 256 + tid; t < first; t += gridDim.x * 256) out[t] = in[t] * A.a.decay;
+    // the tokens before the window: vectors of four where the rows are aligned
+    const int vec = (((uintptr_t)in | (uintptr_t)out) & 15) == 0 ? first & ~3 : 0;
+    for (int t = (blockIdx.x * 256 + tid) * 4; t < vec; t += gridDim.x * 1024)
+        *(f4*)(out + t) = *(const f4*)(in + t) * A.a.decay;
+    for (int t = vec + blockIdx.x * 256 + tid; t < first; t += gridDim.x * 256) out[t] = in[t] * A.a.decay;
     if ((int)blockIdx.x * 1024 >= len - first) return;
     // whole vectors of four tokens where the caller's rows are aligned to them
     const bool wide = (((uintptr_t)(in + first) | (uintptr_t)(out + first)) & 15) == 0;
