@@ -18,8 +18,8 @@
 //                   tokens into one lane, which are the 8 that the same lane
 //                   has to supply as the operand P^T: the weights never leave
 //                   their registers.
-// A lane loads E = DP / 16 values of V for its 8 tokens (neighbours; of 192,
-// eight and four), and the A operand for d = E n + i (i < E) is the i-th of
+// A lane loads E = DP / 16 values of V for its 8 tokens (neighbours; of 192
+// eight and four, of 96 four and two), and the A operand for d = E n + i (i < E) is the i-th of
 // each: the transposition is within a lane, one byte permutation for two values. Nothing goes through
 // LDS but 32 row numbers and scales for each 32 tokens.
 //
@@ -210,7 +210,8 @@ __device__ __forceinline__ void pieces(const float (&x)[8], u4 (&out)[NP]) {
 }
 
 // CT: the cache's type; NQ, NP: pieces of queries and weights; DP: the head
-// size rounded up to 64, 128, 192 or 256; FULL: it is that size.
+// size rounded up to 64, 128, 192 or 256, or 96 itself (16-bit caches); FULL:
+// it is that size.
 // Two workgroups are on a compute unit where their registers fit.
 constexpr int attend_per_cu(int CT, int NQ, int DP) {
     return DP == 256 ? (CT == DQ_I8 && NQ == 1 ? 2 : 1) : DP == 192 ? (NQ == 3 ? 1 : 2) : 2;
@@ -222,10 +223,16 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
     constexpr int EB = CT == DQ_I8 ? 1 : 2;       // bytes of a value
     constexpr int E = DP / 16;                    // values of V a lane loads for a token
     constexpr int VW = E * EB / 4;                // their words
-    constexpr int EA = DP == 192 ? 8 : E;         // of them neighbours; of 192, four more lie past d = 128
+    // of them neighbours; of 96 and 192 the others lie past d = 64 and 128
+    constexpr int EA = DP == 192 ? 8 : DP == 96 ? 4 : E, EX = E - EA;
     constexpr int C = DP / 32;                    // steps of 32 of q . k
     constexpr int KL = DP * EB / 64;              // 16-byte loads of K for 16 tokens
     constexpr int kAcc = DP + 4;
+    // V's loads take whole rows and pass the caches by. K's take 64 bytes of 16
+    // rows: the rest of a line is the next load's, and is mostly better kept
+    // (80 values of 16 bits 42 -> 33 us, 256 of 16 bits 1091 -> 1008, int8 with
+    // weights 316 -> 301), but not for rows of 256 bytes (53 -> 51, 64 -> 61).
+    constexpr bool KSTREAM = FULL && DP == 128 && EB == 2;
     __shared__ AttendScan scan;
     __shared__ int32_t s_row[4][32];
     __shared__ float s_scale[4][64];
@@ -341,7 +348,8 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
 #pragma unroll
                 for (int c = 0; c < KL; ++c) {
                     const int o = c * 64 + g * 16;
-                    kf[h][c] = __builtin_nontemporal_load((const u4*)(p + (FULL || o < row_bytes ? o : 0)));
+                    const u4* x = (const u4*)(p + (FULL || o < row_bytes ? o : 0));
+                    kf[h][c] = KSTREAM ? __builtin_nontemporal_load(x) : *x;
                 }
             }
         };
@@ -436,9 +444,9 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
                 const char* p = (const char*)A.a.v + (size_t)(uint32_t)r * row_bytes;
                 const int o = n16 * EA * EB;
                 load_words<EA * EB / 4>(p + (FULL || o < row_bytes ? o : 0), vf[j]);
-                if constexpr (DP == 192) {
-                    const int o2 = (128 + n16 * 4) * EB;
-                    load_words<EB>(p + (FULL || o2 < row_bytes ? o2 : 0), vf[j] + EA * EB / 4);
+                if constexpr (EX > 0) {
+                    const int o2 = (EA * 16 + n16 * EX) * EB;
+                    load_words<EX * EB / 4>(p + (FULL || o2 < row_bytes ? o2 : 0), vf[j] + EA * EB / 4);
                 }
             }
             issue_fence();
@@ -555,9 +563,9 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int i = 0; i < E; i += 4)
-                    *(f4*)&j_acc[wave][n16 * kAcc + (i < EA ? EA * (4 * g + r) + i : 128 + 4 * (4 * g + r))] =
-                        f4{acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]};
+                for (int i = 0; i < E; i += 2)
+                    *(f2*)&j_acc[wave][n16 * kAcc + (i < EA ? EA * (4 * g + r) + i : EA * 16 + EX * (4 * g + r) + i - EA)] =
+                        f2{acc[i][r], acc[i + 1][r]};
         }
         __syncthreads();
         const bool whole = unit0 == 0 && count == nb;
@@ -642,6 +650,9 @@ AttendKernel attend_i8(dq_dtype q, int D);
 template <int CT, int NQ, int NP>
 AttendKernel attend_pick(int D) {
     if (D <= 64) return D == 64 ? k_attend<CT, NQ, NP, 64, true> : k_attend<CT, NQ, NP, 64, false>;
+    // (80 on tiles of 96 was slower than on tiles of 128)
+    if constexpr (CT != DQ_I8)
+        if (D == 96) return k_attend<CT, NQ, NP, 96, true>;
     if (D <= 128) return D == 128 ? k_attend<CT, NQ, NP, 128, true> : k_attend<CT, NQ, NP, 128, false>;
     if (D <= 192) return D == 192 ? k_attend<CT, NQ, NP, 192, true> : k_attend<CT, NQ, NP, 192, false>;
     return D == 256 ? k_attend<CT, NQ, NP, 256, true> : k_attend<CT, NQ, NP, 256, false>;
