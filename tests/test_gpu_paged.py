@@ -480,6 +480,58 @@ def test_attend_long_sequences(gpu, ct):
     _run(Case(gpu, 1, 1, 8, 64, 64, [20011], "f32", ct, seed=4))
 
 
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 128, 144, 192, 208, 256])
+@pytest.mark.parametrize("qt,ct", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "i8"), ("f32", "i8"), ("f32", "bf16"),
+                                   ("f32", "f16"), ("bf16", "f16"), ("f16", "i8")])
+def test_attend_split_types_and_head_sizes(gpu, dim, qt, ct):
+    """Room for more than 512 tokens: heads are split over workgroups."""
+    log(f"attend split {qt} {ct} dim {dim}")
+    _run(Case(gpu, 4, 1, 3, dim, 16, [700, 0, 1309, 5], qt, ct, seed=dim, scores=dim in (48, 128), per_seq=90))
+
+
+@pytest.mark.parametrize("scores", [False, True])
+@pytest.mark.parametrize("batch,hk,page,lens", [(300, 2, 8, (1, 9, 600, 0, 130)), (700, 1, 16, (33, 0, 0, 257)),
+                                                (513, 1, 1, (3, 5, 0))])
+def test_attend_many_sequences(gpu, batch, hk, page, lens, scores):
+    """More sequences than a workgroup has threads, and more heads than
+    workgroups; short ones whole, longer ones split."""
+    log(f"attend {batch} sequences scores:{scores}")
+    n = [lens[i % len(lens)] for i in range(batch)]
+    _run(Case(gpu, batch, hk, 2, 16, page, n, "bf16", "i8", seed=batch, scores=scores))
+
+
+@pytest.mark.parametrize("scores", [False, True])
+def test_attend_more_units_than_rounds(gpu, scores):
+    """Enough tokens that workers take runs that cross sequences and heads."""
+    log(f"attend runs scores:{scores}")
+    r = np.random.default_rng(7)
+    _run(Case(gpu, 12, 8, 1, 16, 64, [int(x) for x in r.integers(2000, 9000, 12)], "bf16", "bf16", seed=6,
+              scores=scores))
+
+
+@pytest.mark.parametrize("length", [100, 1000])
+def test_attend_many_query_heads_with_weights(gpu, length):
+    """Several tiles of query heads, more than are summed at a time."""
+    log(f"attend 70 heads {length}")
+    _run(Case(gpu, 2, 1, 70, 32, 16, [length, 17], "f32", "f16", seed=length, scores=True))
+    _run(Case(gpu, 2, 1, 70, 32, 16, [length, 17], "bf16", "bf16", seed=length))
+
+
+def test_attend_repeats_bit_for_bit(gpu):
+    """The same call twice gives the same bits: parts are joined in order."""
+    import torch
+
+    log("attend repeats")
+    c = Case(gpu, 6, 2, 4, 64, 16, [3000, 5, 700, 0, 1999, 2500], "bf16", "i8", seed=3, scores=True)
+    try:
+        first = c.attend()
+        for _ in range(5):
+            for a, b in zip(first, c.attend()):
+                assert torch.equal(a, b)
+    finally:
+        c.close()
+
+
 def test_attend_peaked_and_shifted_scores(gpu):
     """One token far above the others, all scores far below zero, growing
     scores (the running maximum moves at every step) and a negative scale."""
@@ -770,7 +822,8 @@ def test_evict(gpu, ct, in_place):
 
 @pytest.mark.parametrize("lens,budget,recent,sinks", [
     ([1, 2, 3], 1, 0, 0), ([40], 39, 0, 0), ([40], 40, 5, 5), ([200, 90], 10, 100, 0),   # more protected than fit
-    ([1100, 1024, 1025], 1024, 128, 4), ([3000], 1500, 0, 1), ([2500, 5], 7, 3, 2)])
+    ([1100, 1024, 1025], 1024, 128, 4), ([3000], 1500, 0, 1), ([2500, 5], 7, 3, 2), ([4097, 4096], 2000, 64, 4),
+    ([8200, 8191, 7000], 4000, 100, 0), ([9001, 2], 8999, 1, 1)])
 @pytest.mark.parametrize("ties", [False, True])
 def test_evict_lengths(gpu, lens, budget, recent, sinks, ties):
     log(f"evict {lens} -> {budget} recent {recent} sinks {sinks} ties {ties}")
@@ -796,6 +849,22 @@ def test_evict_odd_weights(gpu):
 def test_evict_long(gpu):
     log("evict long")
     _evict(gpu, [33000, 9000], 2048, 512, 4, ct="i8", hk=1, dim=16, page=32, seed=5)
+
+
+def test_evict_long_ties(gpu):
+    """Beyond what the registers hold, with equal weights among those that
+    decide and weights of one magnitude."""
+    log("evict long, ties")
+
+    def same(s):
+        s[:] = 0.25
+
+    def near(s):
+        s[:] = 1.0 + s / 64
+
+    _evict(gpu, [34000], 3000, 100, 4, ct="f16", hk=1, dim=16, page=32, seed=6, ties=True, in_place=True)
+    _evict(gpu, [33000, 20000], 9000, 100, 4, ct="f16", hk=1, dim=16, page=32, seed=7, weights=same)
+    _evict(gpu, [33000, 20000], 9000, 100, 4, ct="f16", hk=1, dim=16, page=32, seed=8, weights=near)
 
 
 def test_evict_places_that_do_not_exist(gpu):
