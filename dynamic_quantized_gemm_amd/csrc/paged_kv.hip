@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 //   less), unless they are more than 4096;
 //   the slots below the budget that came free and the slots beyond it that
 //   stay, in order, as two lists.
+// One token over the budget takes one pass instead.
 // A second launch moves the rows, which are most of the traffic, with the whole
 // chip; where at most 64 rows of a head can move (a token at a time over the
 // budget) the first moves them itself.
@@ -328,7 +329,59 @@ struct SelectShared {
     uint32_t a[kSelWaves], b[kSelWaves];
     uint32_t digit, left, ties, count, found;
     uint32_t near[kNear];
+    unsigned long long least[kSelWaves];
 };
+
+// One token over the budget, the steady state of decoding: the least key
+// leaves, of equal ones that in the highest slot, and the token in the slot
+// beyond the budget takes its place. One pass over the keys, whatever their
+// number.
+__device__ __forceinline__ void evict_one(const EvictArgs& A, SelectShared& sh, int item, int b, int n) {
+    const int tid = threadIdx.x;
+    const size_t base = (size_t)item * A.cap;
+    const float* sc = A.scores + base;
+    const int32_t* od = A.order + base;
+    float* sco = A.scores_out + base;
+    int32_t* odo = A.order_out + base;
+    const bool copies = sco != sc || odo != od;
+    const long long recent_from = (long long)A.newest[b] - A.recent;
+    unsigned long long least = ~0ull;
+    constexpr int KG = 8;
+    for (int k0 = 0; k0 < n; k0 += KG * kSelThreads) {
+        float f[KG];
+        int32_t o[KG];
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+            const int i = min(k0 + k * kSelThreads + tid, n - 1);
+            f[k] = sc[i];
+            o[k] = od[i];
+        }
+        issue_fence();
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+            const int i = min(k0 + k * kSelThreads + tid, n - 1);
+            const uint32_t x = evict_key(f[k], o[k], A.sinks, recent_from);
+            least = min(least, (unsigned long long)x << 32 | (0xffffffffu - (uint32_t)i));
+            if (copies && i < A.budget) {
+                sco[i] = f[k];
+                odo[i] = o[k];
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) least = min(least, (unsigned long long)__shfl_xor(least, o));
+    if ((tid & 63) == 0) sh.least[tid >> 6] = least;
+    wait_vmcnt<0>();  // what is copied has arrived before a moved value goes to the same place
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 0; w < kSelWaves; ++w) least = min(least, sh.least[w]);
+        const int slot = (int)(0xffffffffu - (uint32_t)least);
+        int32_t* dst = A.moves + (size_t)A.batch * A.Hk + (size_t)item * 2 * A.moves_stride;
+        dst[0] = slot;
+        dst[A.moves_stride] = A.budget;
+        sh.count = slot < A.budget ? 1 : 0;
+    }
+}
 
 // KPT (a multiple of 4, up to 32): keys a lane holds at a time, runs of four
 // neighbouring slots. MEM: there are more than that, and every pass reads them
@@ -588,7 +641,8 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs
         if (tid == 0) A.moves[item] = 0;
         return;
     }
-    if (n <= KPT * kSelThreads) evict_select<KPT, false>(A, sh, item, b, n);
+    if (n == A.budget + 1) evict_one(A, sh, item, b, n);
+    else if (n <= KPT * kSelThreads) evict_select<KPT, false>(A, sh, item, b, n);
     else if constexpr (KPT == 32) evict_select<KPT, true>(A, sh, item, b, n);
     __syncthreads();
     if (!A.moves_too) {

@@ -851,6 +851,25 @@ def test_evict_long(gpu):
     _evict(gpu, [33000, 9000], 2048, 512, 4, ct="i8", hk=1, dim=16, page=32, seed=5)
 
 
+@pytest.mark.parametrize("n", [2, 65, 1025, 9000, 40001])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_one_token_over(gpu, n, in_place):
+    """The least weight leaves wherever it is: first, last, in the middle, of
+    several equal ones the last; and none but the protected are left."""
+    log(f"evict one of {n} in place:{in_place}")
+
+    def least(at):
+        def put(s):
+            s[:] = s + 0.5
+            s[..., at] = 0.125
+        return put
+
+    for at in ([0], [n - 1], [n // 2], [n // 3, n // 2], [0, n - 1]):
+        _evict(gpu, [n, n - 1], n - 1, 0, 0, dim=16, page=32, hk=1, seed=n, weights=least(at), in_place=in_place)
+    _evict(gpu, [n], n - 1, n // 2, 1, ct="i8", dim=16, page=32, hk=1, seed=n, in_place=in_place)
+    _evict(gpu, [n], n - 1, 2 * n, 0, ct="i8", dim=16, page=32, hk=1, seed=n, in_place=in_place)
+
+
 def test_evict_long_ties(gpu):
     """Beyond what the registers hold, with equal weights among those that
     decide and weights of one magnitude."""
