@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "paged_kv.h"
 
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 // is for the first `sinks` and last `recent` tokens, ties going to the lowest
 // slot. One workgroup of 16 waves selects for one head, each wave a run of
 // slots, so that ballots count in slot order:
-//   the keys, read once and kept in registers up to 32 a lane (beyond 32768
+//   the keys, read once and kept in registers up to 64 a lane (beyond 65536
 //   tokens they are read again for every pass);
 //   the budget-th largest key, 8 bits at a time, from histograms in LDS, of
 //   which there are eight, by lane: weights of one magnitude would otherwise
@@ -383,7 +384,7 @@ __device__ __forceinline__ void evict_one(const EvictArgs& A, SelectShared& sh, 
     }
 }
 
-// KPT (a multiple of 4, up to 32): keys a lane holds at a time, runs of four
+// KPT (a multiple of 4, up to 64): keys a lane holds at a time, runs of four
 // neighbouring slots. MEM: there are more than that, and every pass reads them
 // again, KPT at a time.
 template <int KPT, bool MEM>
@@ -395,6 +396,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     const long long recent_from = (long long)A.newest[b] - A.recent;
     // run k of a lane: slots i0 + 256 k + (0 .. 3); a wave's slots are one run
     constexpr int KV = KPT / 4;
+    typedef typename std::conditional<KPT <= 32, uint32_t, uint64_t>::type Bits;
     const int iters = (n + 4 * kSelThreads - 1) / (4 * kSelThreads);
     const int i0 = wave * iters * 256 + lane * 4;
     // f(k, weights, numbers, how many there are) for the lane's runs k0 + k, up
@@ -529,11 +531,11 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
     auto sort_out = [&](auto f) {
         uint32_t t = tie;
         blocks([&](int k0) {
-            uint32_t kept = 0, under = 0;
+            Bits kept = 0, under = 0;
 #pragma unroll
             for (int k = 0; k < KV; ++k) {
                 const int low = k0 + k < iters ? max(0, min(4, A.budget - (i0 + (k0 + k) * 256))) : 0;
-                under |= ((1u << low) - 1) << (4 * k);
+                under |= (Bits)((1u << low) - 1) << (4 * k);
                 uint32_t before = 0;
                 if (!all_ties) {
 #pragma unroll
@@ -543,7 +545,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t y = x[4 * k + j];
                     const bool stays = all_ties ? y >= prefix : y > prefix || (y == prefix && t + before < left);
-                    kept |= (stays ? 1u : 0u) << (4 * k + j);
+                    kept |= (Bits)(stays ? 1u : 0u) << (4 * k + j);
                     before += y == prefix;
                 }
                 if (!all_ties) {
@@ -554,10 +556,16 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
             f(k0, kept, under);
         });
     };
-    uint32_t holes = 0, movers = 0, kept0 = 0, under0 = 0;
-    sort_out([&](int, uint32_t kept, uint32_t under) {
-        holes += __popc(under & ~kept);
-        movers += __popc(kept & ~under);
+    uint32_t holes = 0, movers = 0;
+    Bits kept0 = 0, under0 = 0;
+    sort_out([&](int, Bits kept, Bits under) {
+        if constexpr (KPT <= 32) {
+            holes += __popc(under & ~kept);
+            movers += __popc(kept & ~under);
+        } else {
+            holes += __popcll(under & ~kept);
+            movers += __popcll(kept & ~under);
+        }
         kept0 = kept;
         under0 = under;
     });
@@ -599,7 +607,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
         for (int j = 0; j < 4; ++j)
             if (bits >> j & 1) to[before++] = i + j;
     };
-    auto put = [&](int k0, uint32_t kept, uint32_t under) {
+    auto put = [&](int k0, Bits kept, Bits under) {
         // weights and numbers of the slots that stay where they are
         if (copies && __ballot(kept & under))
             runs(k0, [&](int k, f4u f, i4u o, int) {
@@ -614,8 +622,8 @@ __device__ __forceinline__ void evict_select(const EvictArgs& A, SelectShared& s
 #pragma unroll
         for (int k = 0; k < KV; ++k) {
             const int i = i0 + (k0 + k) * 256;
-            list(dst, hole0, (under & ~kept) >> (4 * k) & 15u, i);
-            list(src, mover0, (kept & ~under) >> (4 * k) & 15u, i);
+            list(dst, hole0, (uint32_t)((under & ~kept) >> (4 * k)) & 15u, i);
+            list(src, mover0, (uint32_t)((kept & ~under) >> (4 * k)) & 15u, i);
         }
     };
     if (MEM) sort_out(put);
@@ -642,8 +650,11 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs
         return;
     }
     if (n == A.budget + 1) evict_one(A, sh, item, b, n);
-    else if (n <= KPT * kSelThreads) evict_select<KPT, false>(A, sh, item, b, n);
-    else if constexpr (KPT == 32) evict_select<KPT, true>(A, sh, item, b, n);
+    else if (n <= (KPT < 32 ? KPT : 32) * kSelThreads) evict_select<(KPT < 32 ? KPT : 32), false>(A, sh, item, b, n);
+    else if constexpr (KPT == 64) {
+        if (n <= KPT * kSelThreads) evict_select<KPT, false>(A, sh, item, b, n);
+        else evict_select<32, true>(A, sh, item, b, n);
+    }
     __syncthreads();
     if (!A.moves_too) {
         if (tid == 0) A.moves[item] = (int32_t)sh.count;
@@ -989,7 +1000,8 @@ extern "C" int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, in
     const dim3 grid((unsigned)items), block(kSelThreads);
     if (ctx->cap <= 4 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<4>), grid, block, 0, s, A);
     else if (ctx->cap <= 8 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<8>), grid, block, 0, s, A);
-    else hipLaunchKernelGGL((k_kv_evict_select<32>), grid, block, 0, s, A);
+    else if (ctx->cap <= 32 * kSelThreads) hipLaunchKernelGGL((k_kv_evict_select<32>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((k_kv_evict_select<64>), grid, block, 0, s, A);
     DQ_LAUNCH_CHECK("eviction's selection");
     if (!A.moves_too) {
         // workgroups for the most rows that can move, at most 2^14 in all
