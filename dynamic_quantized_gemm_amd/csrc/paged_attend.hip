@@ -169,8 +169,14 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
     }
 }
 
-// Units of 128 tokens that a workgroup takes alone rather than share a head.
-constexpr int kWholeUnits = 4;
+// Up to this many units of 128 tokens a workgroup takes a head alone rather than
+// share it: always up to kWholeUnits, and up to kWholeUnitsMany where the heads
+// alone fill half the chip and two workgroups fit on a compute unit. Microseconds
+// whole and shared, 8 key-value heads of 128: 8 sequences of 250 tokens 8.4 and
+// 11.7, of 500 11.8 and 12.2, of 1000 19.2 and 15.6; 32 of 1000 25.0 and 30.8, on
+// int8 16.3 and 22.4; 160 of up to 1000 on int8 43.8 and 62.1; 80 of 2000 121 and
+// 114. With one workgroup a unit (fp32 on 256 values) 40 of 1000 83 and 73.
+constexpr int kWholeUnits = 4, kWholeUnitsMany = 8;
 
 AttendKernel pick_kernel(const dq_kv_ctx* c) {
     return c->cache_type == DQ_I8 ? attend_i8(c->q_type, c->D)
@@ -217,7 +223,8 @@ int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s) {
     const int64_t items = (int64_t)a.batch * A.Hk * A.tiles;
     // Short sequences are not split: a workgroup takes whole items, finishes
     // them itself and looks up no other sequence's length.
-    A.whole = per_item <= kWholeUnits && (!a.scores || A.tiles == 1);
+    const bool many = items >= c->cus / 2 && c->attend_workers > c->cus;
+    A.whole = per_item <= (many ? kWholeUnitsMany : kWholeUnits) && (!a.scores || A.tiles == 1);
     A.workers = (int)std::min<int64_t>(A.whole ? items : per_item * items, c->attend_workers);
     hipLaunchKernelGGL(pick_kernel(c), dim3((unsigned)A.workers), dim3(256), 0, s, A);
     DQ_LAUNCH_CHECK("attention");

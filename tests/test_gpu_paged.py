@@ -500,6 +500,19 @@ def test_attend_many_sequences(gpu, batch, hk, page, lens, scores):
     _run(Case(gpu, batch, hk, 2, 16, page, n, "bf16", "i8", seed=batch, scores=scores))
 
 
+@pytest.mark.parametrize("qt,ct,dim", [("bf16", "bf16", 64), ("bf16", "i8", 128), ("f32", "f16", 32),
+                                       ("f32", "i8", 256)])
+@pytest.mark.parametrize("batch,per_seq,window", [(15, 64, 0), (16, 64, 0), (16, 65, 0), (16, 130, 1024),
+                                                  (16, 130, 1025), (66, 64, 0)])
+def test_attend_many_heads(gpu, batch, per_seq, window, qt, ct, dim):
+    """Either side of 128 heads, of 1024 slots and of a window of 1024: whole
+    heads of up to eight units, or shared ones; more heads than workgroups."""
+    log(f"attend {batch} sequences of {per_seq} pages window {window} {qt} {ct} {dim}")
+    lens = [16 * per_seq, 0, 1, 1023, 513, 640, 129, 1000, 16 * per_seq - 1]
+    _run(Case(gpu, batch, 8, 2, dim, 16, [lens[i % len(lens)] for i in range(batch)], qt, ct, seed=batch + per_seq,
+              window=window, scores=dim != 64, per_seq=per_seq))
+
+
 @pytest.mark.parametrize("scores", [False, True])
 def test_attend_more_units_than_rounds(gpu, scores):
     """Enough tokens that workers take runs that cross sequences and heads."""
