@@ -10,7 +10,10 @@
 // once (kv_plan.h), whatever the lengths, which only the device knows. A
 // workgroup walks its units; where it holds all of a sequence's units for a
 // head tile it writes the output, else a partial result (maximum, sum,
-// weighted values) that k_attend_join combines.
+// weighted values) that k_attend_finish combines. Where that is faster, a
+// workgroup takes whole heads and gathers their weights itself (`whole`).
+// 131071 tokens of 4 heads of 128 in bf16: 44.5 us, 6.0 TB/s; 32 sequences of
+// up to 4096, 8 heads of 128: 54 us, 6.0 TB/s, of what a copy reaches 6.2.
 //
 // A wave takes 32 of a unit's 128 tokens, on its own until its units end:
 //   S^T = K Q^T     tokens x heads, A = 16 rows of K as they lie in memory;

@@ -79,7 +79,8 @@ DQ_HD void kv_pair(int i, int D, int R, bool interleaved, int* a, int* b) {
 // to within one, whatever the lengths. Up to kKvRound units a worker, all runs
 // are of the same whole number (fewer workers then, none with more to do):
 // runs that begin in the middle of a sequence and end in the next one's cost
-// more than an idle worker.
+// more than an idle worker (108 heads with a window of 1000 tokens 19.7 to 20.1
+// us, shared to within one 23.4).
 constexpr int kKvUnit = 128;
 constexpr int kKvRound = 8;
 

@@ -16,7 +16,9 @@ namespace {
 // the query heads. The workgroups of a key-value head share both out: query
 // heads in turn, runs of 1024 tokens in turn; each finds the sums it needs
 // from the parts itself, so that nothing waits for another workgroup. Parts
-// are added in order, so a result never depends on timing.
+// are added in order, so a result never depends on timing. Bound by latency and
+// its launch where no weights are gathered (4.5 to 5.6 us), else by the kept
+// scores that it reads (48 sequences of up to 20479, 32 heads: 28 us).
 constexpr int kFinishHeads = 64;  // query heads whose sums are kept at a time
 constexpr int kMaxWorkers = 512;  // of k_attend, so the parts of a head
 

@@ -28,8 +28,8 @@ namespace {
 // once for its tokens. For an int8 cache the row's
 // largest magnitude is reduced over those sixteen lanes in registers, so each
 // row is read once and its codes and scale written once.
-// Bound by that traffic: 6001 tokens of 32 + 16 heads of 128 in bf16 27.3 us,
-// 5.4 TB/s, what a plain copy takes.
+// Bound by that traffic: 6001 tokens of 32 + 16 heads of 128 in bf16 25.9 to
+// 27.1 us, 5.4 to 5.7 TB/s; a plain copy of as much takes 26.0 to 26.5 us.
 
 struct AppendArgs {
     const void *q, *k, *v;
@@ -243,11 +243,13 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 //   the budget-th largest key, 8 bits at a time, from histograms in LDS, of
 //   which there are eight, by lane: weights of one magnitude would otherwise
 //   meet in one counter. The keys with the first 8 bits are left in LDS on the
-//   way, and the third and fourth pass look at those alone (32768 tokens: 5 us
-//   less), unless they are more than 4096;
+//   way, and the third and fourth pass look at those alone (32768 tokens: 28.5 to
+//   26.7 us), unless they are more than 4096;
 //   the slots below the budget that came free and the slots beyond it that
 //   stay, in order, as two lists.
-// One token over the budget takes one pass instead.
+// One token over the budget takes one pass instead (32769 tokens of 128 heads:
+// 95 to 18.6 us). Bound by its chain of passes on one compute unit a head: 64
+// heads of up to 32768 tokens 28 us, the moves 25 us, 4.6 TB/s of 256-byte rows.
 // A second launch moves the rows, which are most of the traffic, with the whole
 // chip; where at most 64 rows of a head can move (a token at a time over the
 // budget) the first moves them itself.
@@ -864,7 +866,7 @@ extern "C" int dq_kv_append(dq_kv_ctx* ctx, int64_t tokens, const void* k, int64
     A.R = rope ? rope->R : ctx->D;
     A.geom = ctx->geom;
     // rows per group: as many as leave the chip filled (2^14 groups), at most 4
-    // (6001 tokens of 32 + 16 heads of 128 in bf16: 27.3 us, with 8 30.8)
+    // (6001 tokens of 32 + 16 heads of 128 in bf16: 27.3 us when chosen, with 8 30.8)
     const int64_t rows = A.Hq + 2 * (int64_t)A.Hk;
     int chunk = 1;
     while (chunk < 4 && tokens * (rows / (2 * chunk)) >= (1 << 14)) chunk *= 2;
@@ -993,7 +995,8 @@ extern "C" int dq_kv_evict(dq_kv_ctx* ctx, int batch, int budget, int recent, in
     const hipStream_t s = (hipStream_t)stream;
     const int items = batch * ctx->Hk;
     // the most rows of a head that can move. A workgroup moves 64 by itself in
-    // less than a second launch takes; lens_out is then written while other
+    // less than a second launch takes (one over 1024, 128 heads: 8.1 us, with
+    // the launch 12.1); lens_out is then written while other
     // heads still read lens, so not where they are one tensor
     const int most = std::max(0, std::min(budget, ctx->cap - budget));
     A.moves_too = most <= 64 && lens_out != lens;
