@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(256) k_kv_read(const ReadArgs A) {
 // ---------------------------------------------------------------- eviction
 //
 // Of a head's n > budget tokens those with the `budget` largest keys stay,
-// where a key is the gathered weight as an ordered integer, the largest there
-// is for the first `sinks` and last `recent` tokens, ties going to the lowest
+// where a key is the gathered weight as an ordered integer, one above all weights
+// for the first `sinks` and last `recent` tokens, ties going to the lowest
 // slot. One workgroup of 16 waves selects for one head, each wave a run of
 // slots, so that ballots count in slot order:
 //   the keys, read once and kept in registers up to 64 a lane (beyond 65536
@@ -275,9 +275,9 @@ struct EvictArgs {
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
 
 __device__ __forceinline__ uint32_t evict_key(float score, int order, int sinks, long long recent_from) {
-    if (order < sinks || order > recent_from) score = __builtin_inff();
+    if (order < sinks || order > recent_from) return 0xffffffffu;  // stays before any weight, NaN and infinity too
     const uint32_t k = f2ord(score);
-    return score != score ? 0xffffffffu : k;  // a NaN is the largest
+    return score != score ? 0xfffffffeu : k;  // a NaN is the largest weight
 }
 
 // Up to R rows of keys, values, scales, weights and numbers by sixteen lanes:

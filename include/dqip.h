@@ -738,8 +738,8 @@ void dq_rope_release(dq_rope_ctx* ctx);
  * `budget` tokens. Of its slots [0, len) those with order < sinks or order >
  * newest[b] - recent stay first (order: the token's running number, int32
  * [batch, kv_heads, cap]; newest int32 [batch]), then those of the largest
- * scores ([batch, kv_heads, cap] fp32, a NaN above everything; ties, and more
- * such tokens than fit, go to the lowest slot). Kept tokens at slots from
+ * scores ([batch, kv_heads, cap] fp32, a NaN above every other score; ties, and
+ * more protected tokens than fit, go to the lowest slot). Kept tokens at slots from
  * budget on move, in order, into the slots below it that came free: rows and
  * scales in the cache, scores and order into scores_out and order_out, whose
  * entries from the new length on are left alone. lens_out = min(len, budget).

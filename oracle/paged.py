@@ -93,8 +93,8 @@ def evict_source(scores, order, n, budget, newest, recent, sinks):
     safe = [order[i] < sinks or int(order[i]) > int(newest) - recent for i in range(n)]
 
     def key(i):
-        w = np.inf if safe[i] else float(scores[i])
-        return (0, 0.0, i) if w != w else (1, -w, i)  # a NaN above everything
+        w = float(scores[i])
+        return (0, 0.0, i) if safe[i] else (1, 0.0, i) if w != w else (2, -w, i)  # a NaN above every other weight
 
     kept = set(sorted(range(n), key=key)[:budget])
     movers = [i for i in sorted(kept) if i >= budget]
