@@ -212,6 +212,21 @@ __device__ __forceinline__ void pieces(const float (&x)[8], u4 (&out)[NP]) {
     }
 }
 
+// Of each value its first piece that is not 0, which has its sign (the others can
+// be 0 or of the other sign). magnitude: 0x7fff.
+template <int NP>
+__device__ __forceinline__ u4 lead_piece(const u4 (&p)[NP], uint32_t magnitude) {
+    u4 r = p[0];
+#pragma unroll
+    for (int i = 1; i < NP; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t keep = (r[w] & magnitude ? 0xffffu : 0u) | (r[w] & magnitude << 16 ? 0xffff0000u : 0u);
+            r[w] = (r[w] & keep) | (p[i][w] & ~keep);
+        }
+    return r;
+}
+
 // CT: the cache's type; NQ, NP: pieces of queries and weights; DP: the head
 // size rounded up to 64, 128, 192 or 256, or 96 itself (16-bit caches); FULL:
 // it is that size.
@@ -455,12 +470,17 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
             issue_fence();
             // ---- scores
             f4 s[2] = {f4{0, 0, 0, 0}, f4{0, 0, 0, 0}};
+            // h's 16 tokens and 32 values of d (int8: 64) of K
+            auto keys = [&](int h, int c) {
+                u4 x = kf[h][c];
+                if (!FULL && c * 64 + g * 16 >= row_bytes) x = u4{0, 0, 0, 0};
+                return x;
+            };
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int c = 0; c < KL; ++c) {
-                    u4 x = kf[h][c];
-                    if (!FULL && c * 64 + g * 16 >= row_bytes) x = u4{0, 0, 0, 0};
+                    const u4 x = keys(h, c);
                     if constexpr (CT == DQ_I8) {
                         const u2 a = codes_bf16x4(x[0]), e = codes_bf16x4(x[1]), i = codes_bf16x4(x[2]),
                                  o = codes_bf16x4(x[3]);
@@ -474,6 +494,30 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
                         for (int p = 0; p < NQ; ++p) s[h] = Ops::mfma(x, q[c][p], s[h]);
                     }
                 }
+            if constexpr (NQ > 1 && CT != DQ_I8) {
+                // Times an infinite key the pieces of one value can be of both
+                // signs or 0, and their sum a NaN where the product is infinite:
+                // a score that is not finite is taken from one piece a value (one
+                // such leaves no finite sum of the eight). The check costs 4 x
+                // 400 tokens of 8 heads of 64, fp32 on bf16, 8.1 to 8.4 us, with
+                // 128 values or 32 x 3000 tokens nothing.
+                auto finite = [](float y) { return __builtin_fabsf(y) < __builtin_inff(); };
+                const f4 sum = s[0] + s[1];
+                if (__builtin_expect(__ballot(!finite((sum[0] + sum[1]) + (sum[2] + sum[3]))) != 0, 0)) {
+                    // (found here when they are needed: kept through the loop
+                    // they would take 4 C registers)
+                    uint32_t magnitude = 0x7fffu;
+                    asm volatile("" : "+s"(magnitude));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        f4 y = {0, 0, 0, 0};
+#pragma unroll
+                        for (int c = 0; c < KL; ++c) y = Ops::mfma(keys(h, c), lead_piece<NQ>(q[c], magnitude), y);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[h][r] = finite(s[h][r]) ? s[h][r] : y[r];
+                    }
+                }
+            }
             // ---- weights
             float x[8];
 #pragma unroll

@@ -726,7 +726,10 @@ void dq_rope_release(dq_rope_ctx* ctx);
  *   s_t = sm_scale q . k_t,  p = softmax(s),  out = sum_t p_t v_t,
  *   lse = log sum_t exp(s_t)     ([batch, q_heads] fp32, may be NULL)
  * No token (or only weights of zero): out 0, lse -infinity. Sums and softmax
- * are fp32; a NaN or infinity in a row outside the range has no effect.
+ * are fp32; a NaN or infinity in a row outside the range has no effect. In the
+ * range a token whose score is -infinity weighs nothing; a score of +infinity
+ * or NaN shows as NaN. (On an int8 cache an infinity in an fp32 or fp16 query
+ * counts as NaN, in fp32 also a value that bf16 rounds to one.)
  * scores and scores_out ([batch, kv_heads, cap] fp32, both or neither, may be
  * the same): for t < len
  *   scores_out = decay * scores + the sum of p_t over the query heads of the
