@@ -816,20 +816,42 @@ def dq_lstm_release(ctx):
 
 # -------------------------------------- rotary positions, paged cache
 
-def _dev(t, what, nbytes):
-    """_ptr for calls that take many small tensors: what passes the checks
-    passes them in a third of the time, the rest is _ptr's to name."""
+# what these calls check a tensor's type by: dq_dtype codes, and two of the
+# binding's own (indexes, lengths and positions; not checked)
+_I32, _ANY = 5, 6
+_TORCH = [None] * 7  # their torch dtypes, filled when the first tensor is checked
+
+
+def _same_type(t, what, type_):
+    """Refuses a tensor that the kernels would read as elements of another
+    type: by the size of its elements, and by its dtype where that is one the
+    calls know (of another, a view of the same bytes, the size is all)."""
+    if _TORCH[_I32] is None:
+        import torch
+
+        _TORCH[DQ_F32], _TORCH[DQ_BF16], _TORCH[DQ_F16] = torch.float32, torch.bfloat16, torch.float16
+        _TORCH[DQ_I8], _TORCH[_I32] = torch.int8, torch.int32
+    if t.element_size() != _ELEM.get(type_, 4) or (t.dtype in _TORCH and t.dtype is not _TORCH[type_]):
+        raise DQError(DQ_ERR_TYPE, what, f"{_TORCH[type_]} expected, got {t.dtype}")
+
+
+def _dev(t, what, nbytes, type_):
+    """_ptr for calls that take many small tensors, with their type:
+    what passes the checks passes them in a third of the time, the rest is
+    _ptr's to name."""
     if t is None:
         return None
     try:
-        if t.is_cuda and t.nbytes >= nbytes and t.is_contiguous():
+        if t.dtype is _TORCH[type_] and t.is_cuda and t.nbytes >= nbytes and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
+    if type_ != _ANY and not isinstance(t, int):
+        _same_type(t, what, type_)
     return _ptr(t, what, nbytes)
 
 
-def _rows(t, what, heads, dim, elem, tokens=None):
+def _rows(t, what, heads, dim, elem, tokens=None, type_=_ANY):
     """(pointer, token stride, head stride) of a [tokens, heads, dim] device
     tensor whose rows of dim are dense; tokens and heads may be strided."""
     shape = t.shape
@@ -841,8 +863,11 @@ def _rows(t, what, heads, dim, elem, tokens=None):
     ts, hs, ds = t.stride()
     if ds != 1 and dim > 1:
         raise DQError(DQ_ERR_ARG, what, "the last dimension must be dense")
-    if t.element_size() != elem:
-        raise DQError(DQ_ERR_ARG, what, f"elements of {elem} bytes expected")
+    if t.dtype is not _TORCH[type_]:
+        if t.element_size() != elem:
+            raise DQError(DQ_ERR_ARG, what, f"elements of {elem} bytes expected")
+        if type_ != _ANY:
+            _same_type(t, what, type_)
     return t.data_ptr(), ts, hs
 
 
@@ -880,11 +905,13 @@ def dq_rope_forward(ctx, x, positions, y, inverse=False, type_=None, stream=None
         type_ = _ROPE_TYPES.get(str(x.dtype))
         if type_ is None:
             raise DQError(DQ_ERR_TYPE, w, f"{x.dtype} is not supported")
+    elif type_ not in _ELEM:
+        raise DQError(DQ_ERR_TYPE, w, f"no type {type_}")
     n, heads = int(x.shape[0]), int(x.shape[1]) if len(x.shape) == 3 else -1
-    elem = _ELEM.get(type_, 0)
-    xp, xt, xh = _rows(x, w, heads, dim, elem)
-    yp, yt, yh = _rows(y, w, heads, dim, elem, n)
-    _check(load().dq_rope_forward(ctx, xp, type_, n, heads, xt, xh, _dev(positions, w, 4 * axes * n), yp, yt, yh,
+    elem = _ELEM[type_]
+    xp, xt, xh = _rows(x, w, heads, dim, elem, type_=type_)
+    yp, yt, yh = _rows(y, w, heads, dim, elem, n, type_)
+    _check(load().dq_rope_forward(ctx, xp, type_, n, heads, xt, xh, _dev(positions, w, 4 * axes * n, _I32), yp, yt, yh,
                                   1 if inverse else 0, _stream(stream)), w)
 
 
@@ -900,8 +927,9 @@ def dq_rope_release(ctx):
 
 # sizes of each context made by dq_kv_init: (batch, q_heads, kv_heads,
 # head_dim, pages_per_seq, slots of a sequence, bytes of a query element,
-# bytes of the cache, bytes of its scales)
+# bytes of the cache, bytes of its scales); its types: (queries, cache)
 _KV_DIMS = {}
+_KV_TYPES, _UNTYPED = {}, (_ANY, _ANY)
 
 
 def dq_kv_init(batch, q_heads, kv_heads, head_dim, pages, page_size, pages_per_seq, q_type, cache_type,
@@ -915,6 +943,7 @@ def dq_kv_init(batch, q_heads, kv_heads, head_dim, pages, page_size, pages_per_s
     _KV_DIMS[h.value] = (int(batch), int(q_heads), int(kv_heads), int(head_dim), int(pages_per_seq),
                          int(pages_per_seq) * int(page_size), _ELEM[q_type], rows * int(head_dim) * _ELEM[cache_type],
                          4 * rows)
+    _KV_TYPES[h.value] = (q_type, cache_type)
     return h.value
 
 
@@ -925,9 +954,9 @@ def _kv_dims(ctx, what):
     return d
 
 
-def _kv_cache(d, what, seqs, block_table, k_cache, v_cache, k_scale, v_scale):
-    return (_dev(block_table, what, 4 * seqs * d[4]), _dev(k_cache, what, d[7]), _dev(v_cache, what, d[7]),
-            _dev(k_scale, what, d[8]), _dev(v_scale, what, d[8]))
+def _kv_cache(d, ct, what, seqs, block_table, k_cache, v_cache, k_scale, v_scale):
+    return (_dev(block_table, what, 4 * seqs * d[4], _I32), _dev(k_cache, what, d[7], ct), _dev(v_cache, what, d[7], ct),
+            _dev(k_scale, what, d[8], DQ_F32), _dev(v_scale, what, d[8], DQ_F32))
 
 
 def dq_kv_append(ctx, k, v, index, block_table, k_cache, v_cache, k_scale=None, v_scale=None, seq_ids=None, q=None,
@@ -938,22 +967,24 @@ def dq_kv_append(ctx, k, v, index, block_table, k_cache, v_cache, k_scale=None, 
     context `rope` at positions [axes, tokens]."""
     w = "dq_kv_append"
     d = _kv_dims(ctx, w)
+    qt, ct = _KV_TYPES.get(ctx, _UNTYPED)
     n = int(k.shape[0])
-    kp, kt, kh = _rows(k, w, d[2], d[3], d[6])
-    vp, vt, vh = _rows(v, w, d[2], d[3], d[6], n)
-    qp, qt, qh, op, pp = None, 0, 0, None, None
+    kp, kt, kh = _rows(k, w, d[2], d[3], d[6], type_=qt)
+    vp, vt, vh = _rows(v, w, d[2], d[3], d[6], n, qt)
+    qp, qs, qh, op, pp = None, 0, 0, None, None
     if q is not None:
-        qp, qt, qh = _rows(q, w, d[1], d[3], d[6], n)
-        op = _dev(q_out, w, n * d[1] * d[3] * d[6])
+        qp, qs, qh = _rows(q, w, d[1], d[3], d[6], n, qt)
+        op = _dev(q_out, w, n * d[1] * d[3] * d[6], qt)
     if rope is not None:
         if rope not in _ROPE_DIMS:
             raise DQError(DQ_ERR_STATE, w, "no rotary context")
-        pp = _dev(positions, w, 4 * _ROPE_DIMS[rope][1] * n)
+        pp = _dev(positions, w, 4 * _ROPE_DIMS[rope][1] * n, _I32)
     elif positions is not None:
         raise DQError(DQ_ERR_ARG, w, "rope and positions go together")
-    _check(load().dq_kv_append(ctx, n, kp, kt, kh, vp, vt, vh, _dev(index, w, 4 * n), _dev(seq_ids, w, 4 * n),
-                               *_kv_cache(d, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
-                               qp, qt, qh, op, rope, pp, _stream(stream)), w)
+    _check(load().dq_kv_append(ctx, n, kp, kt, kh, vp, vt, vh, _dev(index, w, 4 * n, _I32),
+                               _dev(seq_ids, w, 4 * n, _I32),
+                               *_kv_cache(d, ct, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
+                               qp, qs, qh, op, rope, pp, _stream(stream)), w)
 
 
 def dq_kv_read(ctx, index, block_table, k_cache, v_cache, k_scale=None, v_scale=None, k_out=None, v_out=None,
@@ -962,11 +993,12 @@ def dq_kv_read(ctx, index, block_table, k_cache, v_cache, k_scale=None, v_scale=
     as values, to k_out and v_out [tokens, kv_heads, head_dim]."""
     w = "dq_kv_read"
     d = _kv_dims(ctx, w)
+    qt, ct = _KV_TYPES.get(ctx, _UNTYPED)
     n = int(index.numel())
     size = n * d[2] * d[3] * d[6]
-    _check(load().dq_kv_read(ctx, n, _dev(index, w, 4 * n), _dev(seq_ids, w, 4 * n),
-                             *_kv_cache(d, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
-                             _dev(k_out, w, size), _dev(v_out, w, size), _stream(stream)), w)
+    _check(load().dq_kv_read(ctx, n, _dev(index, w, 4 * n, _I32), _dev(seq_ids, w, 4 * n, _I32),
+                             *_kv_cache(d, ct, w, d[0], block_table, k_cache, v_cache, k_scale, v_scale),
+                             _dev(k_out, w, size, qt), _dev(v_out, w, size, qt), _stream(stream)), w)
 
 
 def dq_kv_attend(ctx, q, lens, block_table, k_cache, v_cache, k_scale, v_scale, out, sm_scale, lse=None, window=0,
@@ -976,13 +1008,15 @@ def dq_kv_attend(ctx, q, lens, block_table, k_cache, v_cache, k_scale, v_scale, 
     and scores_out [batch, kv_heads, pages_per_seq * page_size] fp32."""
     w = "dq_kv_attend"
     d = _kv_dims(ctx, w)
+    qt, ct = _KV_TYPES.get(ctx, _UNTYPED)
     n = int(q.shape[0])
-    qp, qt, qh = _rows(q, w, d[1], d[3], d[6])
+    qp, qs, qh = _rows(q, w, d[1], d[3], d[6], type_=qt)
     size = 4 * n * d[2] * d[5]
-    _check(load().dq_kv_attend(ctx, n, qp, qt, qh, _dev(lens, w, 4 * n),
-                               *_kv_cache(d, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
-                               _dev(out, w, n * d[1] * d[3] * d[6]), sm_scale, _dev(lse, w, 4 * n * d[1]), window,
-                               _dev(scores, w, size), _dev(scores_out, w, size), decay, _stream(stream)), w)
+    _check(load().dq_kv_attend(ctx, n, qp, qs, qh, _dev(lens, w, 4 * n, _I32),
+                               *_kv_cache(d, ct, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
+                               _dev(out, w, n * d[1] * d[3] * d[6], qt), sm_scale,
+                               _dev(lse, w, 4 * n * d[1], DQ_F32), window, _dev(scores, w, size, DQ_F32),
+                               _dev(scores_out, w, size, DQ_F32), decay, _stream(stream)), w)
 
 
 def dq_kv_evict(ctx, budget, lens, newest, scores, order, block_table, k_cache, v_cache, k_scale, v_scale,
@@ -991,13 +1025,14 @@ def dq_kv_evict(ctx, budget, lens, newest, scores, order, block_table, k_cache, 
     lens, newest int32 [batch]; the outputs may be their inputs."""
     w = "dq_kv_evict"
     d = _kv_dims(ctx, w)
+    _, ct = _KV_TYPES.get(ctx, _UNTYPED)
     n = int(lens.numel())
     size = 4 * n * d[2] * d[5]
-    _check(load().dq_kv_evict(ctx, n, int(budget), int(recent), int(sinks), _dev(lens, w, 4 * n),
-                              _dev(newest, w, 4 * n), _dev(scores, w, size), _dev(order, w, size),
-                              *_kv_cache(d, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
-                              _dev(scores_out, w, size), _dev(order_out, w, size), _dev(lens_out, w, 4 * n),
-                              _stream(stream)), w)
+    _check(load().dq_kv_evict(ctx, n, int(budget), int(recent), int(sinks), _dev(lens, w, 4 * n, _I32),
+                              _dev(newest, w, 4 * n, _I32), _dev(scores, w, size, DQ_F32), _dev(order, w, size, _I32),
+                              *_kv_cache(d, ct, w, n, block_table, k_cache, v_cache, k_scale, v_scale),
+                              _dev(scores_out, w, size, DQ_F32), _dev(order_out, w, size, _I32),
+                              _dev(lens_out, w, 4 * n, _I32), _stream(stream)), w)
 
 
 def dq_kv_take_errors(ctx, stream=None) -> int:
@@ -1014,4 +1049,5 @@ def dq_kv_info(ctx):
 
 def dq_kv_release(ctx):
     _KV_DIMS.pop(ctx, None)
+    _KV_TYPES.pop(ctx, None)
     load().dq_kv_release(ctx)
