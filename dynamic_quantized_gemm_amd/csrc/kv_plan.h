@@ -4,6 +4,7 @@
 // use (no HIP header is needed).
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #if defined(__HIPCC__)
@@ -69,6 +70,16 @@ DQ_HD void kv_pair(int i, int D, int R, bool interleaved, int* a, int* b) {
         *a = R + (i - R / 2);
         *b = *a + (D - R) / 2;
     }
+}
+
+// A rotary pair's frequency in turns, f / 2 pi = hi + lo to 2^-103 of it (1 / 2 pi
+// is its double and the rest's; the product's own rest by fma). Times a position
+// of 31 bits that is 3e-14 of a turn for the largest frequency, 1e9, and 4e-23 for
+// those up to 1.
+inline void kv_turns(double f, double* hi, double* lo) {
+    const double c0 = 0x1.45f306dc9c883p-3, c1 = -0x1.6b01ec5417056p-57;
+    *hi = f * c0;
+    *lo = fma(f, c0, -*hi) + f * c1;
 }
 
 // ------------------------------------------------------- sharing out tokens

@@ -151,9 +151,11 @@ __device__ __forceinline__ void store4_any(void* p, int type, size_t i, f4 f) {
     else *(h4*)((_Float16*)p + i) = __builtin_convertvector(f, h4);
 }
 
-// cos and sin of pos * freq (freq in turns, hi + lo). The product is reduced
-// to a fraction of a turn in fp64 with its remainder kept, so a position of 31
-// bits loses nothing, and the Taylor series on [-pi/4, pi/4] (first term left
+// cos and sin of pos * freq (freq in turns, hi + lo, from kv_turns). The product
+// is reduced to a fraction of a turn in fp64 with its remainder kept: a position
+// of 31 bits is off by 1e-16 of a turn with frequencies up to 1 and by 3e-14 with
+// the largest, 1e9 (n is the rounded product's then, so r can be some 70 turns).
+// The Taylor series on [-pi/4, pi/4] (first term left
 // out: x^17 / 17! < 5e-17) are summed in fp64, whose rate on this chip is
 // fp32's: the results are fp32 values rounded once.
 __device__ __forceinline__ void rope_cos_sin(int pos, double2 freq, float* c, float* s) {

@@ -163,11 +163,7 @@ extern "C" int dq_rope_init(dq_rope_ctx** ctx, int head_dim, int rotary_dim, con
         axes = std::max(axes, axis_of_pair[i] + 1);
     }
     double2 freq[DQ_ROPE_DIM_MAX / 2];
-    for (int i = 0; i < P; ++i) {
-        const long double turns = (long double)inv_freq[i] / 6.283185307179586476925286766559L;
-        freq[i].x = (double)turns;
-        freq[i].y = (double)(turns - (long double)freq[i].x);
-    }
+    for (int i = 0; i < P; ++i) kv_turns(inv_freq[i], &freq[i].x, &freq[i].y);
     dq_rope_ctx* c = new (std::nothrow) dq_rope_ctx();
     if (!c) DQ_FAIL(DQ_ERR_ALLOC, "host allocation for the rotary context failed");
     (void)hipGetDevice(&c->device);

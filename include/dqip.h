@@ -636,9 +636,10 @@ void dq_lstm_release(dq_lstm_ctx* ctx);
  * interleaved != 0; elements from rotary_dim on pass through. inverse != 0
  * turns by the opposite angle: the rotation is orthogonal, so that is also
  * the gradient's pass (the gradient of x from that of y). The angle is the
- * exact product reduced to one turn in fp64, cos and sin are rounded to fp32
- * once; the rotation is fp32 (two products, then their sum) and rounded to
- * x's type once.
+ * product reduced to one turn in fp64 with its remainder (any position: to 1e-15
+ * radians for frequencies up to 1, to 3e-13 for the largest), cos and sin are
+ * rounded to fp32 once; the rotation is fp32 (two products, then their sum) and
+ * rounded to x's type once.
  *
  * dq_rope_init: head_dim, rotary_dim even, 2 <= rotary_dim <= head_dim <=
  * DQ_ROPE_DIM_MAX; axis_of_pair (HOST, rotary_dim / 2 values in [0,
