@@ -179,6 +179,12 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
 // int8 16.3 and 22.4; 160 of up to 1000 on int8 43.8 and 62.1; 80 of 2000 121 and
 // 114. With one workgroup a unit (fp32 on 256 values) 40 of 1000 83 and 73.
 constexpr int kWholeUnits = 4, kWholeUnitsMany = 8;
+// With weights gathered, tokens that a sequence can hold before the window: a
+// whole head decays their weights with its one workgroup, the finish with the
+// chip. Whole and shared, int8, 8 heads of 128, window 512: 8 sequences of 4500
+// slots 13.1 and 13.9, of 8500 15.5 and 14.3; window 1000: 32 of 4500 25.4 and
+// 25.7, 64 of 4500 38.1 and 36.6; one of 131072, window 512: 73.5 and 14.5.
+constexpr int kWholeBefore = 4096;
 
 AttendKernel pick_kernel(const dq_kv_ctx* c) {
     return c->cache_type == DQ_I8 ? attend_i8(c->q_type, c->D)
@@ -226,7 +232,9 @@ int dq_launch_attend(const dq_kv_ctx* c, const DqAttendArgs& a, hipStream_t s) {
     // Short sequences are not split: a workgroup takes whole items, finishes
     // them itself and looks up no other sequence's length.
     const bool many = items >= c->cus / 2 && c->attend_workers > c->cus;
-    A.whole = per_item <= (many ? kWholeUnitsMany : kWholeUnits) && (!a.scores || A.tiles == 1);
+    const int before = a.window > 0 ? std::max(0, c->cap - a.window) : 0;
+    A.whole = per_item <= (many ? kWholeUnitsMany : kWholeUnits) &&
+              (!a.scores || (A.tiles == 1 && before <= kWholeBefore));
     A.workers = (int)std::min<int64_t>(A.whole ? items : per_item * items, c->attend_workers);
     hipLaunchKernelGGL(pick_kernel(c), dim3((unsigned)A.workers), dim3(256), 0, s, A);
     DQ_LAUNCH_CHECK("attention");
