@@ -71,11 +71,11 @@ template <> struct Elem<DQ_BF16> { typedef __bf16 S; };
 template <> struct Elem<DQ_F16> { typedef _Float16 S; };
 template <> struct Elem<DQ_I8> { typedef int8_t S; };
 
-// N elements of type S moved as one aligned access where N * sizeof(S) is a
-// power of two up to 16 bytes.
-template <typename S, int N>
+// N elements of type S moved as one access, N * sizeof(S) a power of two up to 16
+// bytes. ALIGN: what p is aligned to, the access's own size unless given.
+template <typename S, int N, int ALIGN = N * (int)sizeof(S)>
 __device__ __forceinline__ void load_vec(const S* p, float (&f)[N]) {
-    typedef S V __attribute__((ext_vector_type(N)));
+    typedef S V __attribute__((ext_vector_type(N), aligned(ALIGN)));
     const V v = *(const V*)p;
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = (float)v[i];
@@ -85,9 +85,9 @@ __device__ __forceinline__ void load_vec(const S* p, float (&f)[1]) { f[0] = (fl
 
 // Stores past the caches: the rotation of 168 MB took 37.5 us with them and 43
 // without, a prompt's append 34 and 46, small ones the same.
-template <typename S, int N>
+template <typename S, int N, int ALIGN = N * (int)sizeof(S)>
 __device__ __forceinline__ void store_vec(S* p, const float (&f)[N]) {
-    typedef S V __attribute__((ext_vector_type(N)));
+    typedef S V __attribute__((ext_vector_type(N), aligned(ALIGN)));
     V v;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = (S)f[i];
@@ -96,12 +96,13 @@ __device__ __forceinline__ void store_vec(S* p, const float (&f)[N]) {
 template <typename S>
 __device__ __forceinline__ void store_vec(S* p, const float (&f)[1]) { *p = (S)f[0]; }
 
-// VP pairs of a row: VP elements from lo and from hi, or 2 VP neighbours from lo.
+// VP pairs of a row: VP elements from lo and from hi, or 2 VP neighbours from lo;
+// aligned to VP elements or 2 VP neighbours, a single pair to its elements alone.
 template <typename S, int VP, bool IL>
 __device__ __forceinline__ void load_pairs(const S* row, int lo, int hi, float (&a)[VP], float (&b)[VP]) {
     if constexpr (IL) {
         float e[2 * VP];
-        load_vec(row + lo, e);
+        load_vec<S, 2 * VP, (VP > 1 ? 2 * VP : 1) * (int)sizeof(S)>(row + lo, e);
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
             a[i] = e[2 * i];
@@ -122,7 +123,7 @@ __device__ __forceinline__ void store_pairs(S* row, int lo, int hi, const float 
             e[2 * i] = a[i];
             e[2 * i + 1] = b[i];
         }
-        store_vec(row + lo, e);
+        store_vec<S, 2 * VP, (VP > 1 ? 2 * VP : 1) * (int)sizeof(S)>(row + lo, e);
     } else {
         store_vec(row + lo, a);
         store_vec(row + hi, b);
