@@ -131,12 +131,6 @@ __device__ __forceinline__ void store_pairs(S* row, int lo, int hi, const float 
 }
 
 // Element i of a tensor whose type is known at run time.
-__device__ __forceinline__ float load_any(const void* p, int type, long long i) {
-    if (type == DQ_F32) return ((const float*)p)[i];
-    if (type == DQ_BF16) return (float)((const __bf16*)p)[i];
-    if (type == DQ_F16) return (float)((const _Float16*)p)[i];
-    return (float)((const int8_t*)p)[i];
-}
 __device__ __forceinline__ void store_any(void* p, int type, long long i, float f) {
     if (type == DQ_F32) ((float*)p)[i] = f;
     else if (type == DQ_BF16) ((__bf16*)p)[i] = (__bf16)f;
