@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(kSelThreads) k_kv_evict_select(const EvictArgs
     if (A.moves_too && h == 0 && tid == 0) A.lens_out[b] = min(n, A.budget);
     if (n <= A.budget) {
         const size_t base = (size_t)item * A.cap;
-        for (int i = tid; i < n; i += kSelThreads) {
+        const bool copies = A.scores_out != A.scores || A.order_out != A.order;
+        for (int i = tid; copies && i < n; i += kSelThreads) {
             A.scores_out[base + i] = A.scores[base + i];
             A.order_out[base + i] = A.order[base + i];
         }
