@@ -694,7 +694,8 @@ void dq_rope_release(dq_rope_ctx* ctx);
  * DQ_F16 / DQ_I8), each with each. gather_scores != 0 lets dq_kv_attend gather
  * weights (batch * q_heads * cap fp32 more of workspace; cap * q_heads /
  * kv_heads below 2^29 - 192 then). Allocates every device buffer of the
- * context (none later). Errors: DQ_ERR_ARG, DQ_ERR_TYPE,
+ * context (none later), with or without evictions their lists of batch *
+ * kv_heads * cap int32 among them. Errors: DQ_ERR_ARG, DQ_ERR_TYPE,
  * DQ_ERR_RANGE, DQ_ERR_ALLOC, DQ_ERR_HIP.
  *
  * All calls are asynchronous on `stream` and allocate nothing. dq_kv_attend
@@ -736,7 +737,9 @@ void dq_rope_release(dq_rope_ctx* ctx);
  *   scores_out = decay * scores + the sum of p_t over the query heads of the
  * key-value head (p_t = 0 before the window); other entries are left alone.
  * A page that does not exist, or a length out of range: out and lse of the
- * sequence's heads that need it are NaN.
+ * sequence's heads that need it are NaN, and so are the gathered weights of the
+ * tokens that a bad page's key-value head attends to; a length out of range
+ * leaves scores_out alone.
  *
  * dq_kv_evict: every head of a sequence with len > budget is cut down to
  * `budget` tokens. Of its slots [0, len) those with order < sinks or order >
@@ -748,7 +751,8 @@ void dq_rope_release(dq_rope_ctx* ctx);
  * scales in the cache, scores and order into scores_out and order_out, whose
  * entries from the new length on are left alone. lens_out = min(len, budget).
  * scores_out, order_out and lens_out may be their inputs. The budget is >= 1.
- * A move from or to a page that does not exist leaves the cache's row alone.
+ * A move from or to a page that does not exist leaves the cache's row alone; a
+ * length out of range counts as the nearest end of [0, cap].
  *
  * dq_kv_take_errors: how many such places the calls before it met (as their
  * kernels counted them: one place can count more than once), and clears the
