@@ -275,9 +275,9 @@ struct EvictArgs {
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
 
 __device__ __forceinline__ uint32_t evict_key(float score, int order, int sinks, long long recent_from) {
-    if (order < sinks || order > recent_from) return 0xffffffffu;  // stays before any weight, NaN and infinity too
-    const uint32_t k = f2ord(score);
-    return score != score ? 0xfffffffeu : k;  // a NaN is the largest weight
+    const uint32_t k = score != score ? 0xfffffffeu : f2ord(score);  // a NaN is the largest weight
+    // (both compared, no branch: with one, 100000 tokens of 8 heads take 176 us, not 167)
+    return (order < sinks) | (order > recent_from) ? 0xffffffffu : k;  // stays before any weight
 }
 
 // Up to R rows of keys, values, scales, weights and numbers by sixteen lanes:
