@@ -659,6 +659,7 @@ __global__ void __launch_bounds__(256, attend_per_cu(CT, NQ, DP)) k_attend(const
             // back by others, once all of them have reached the L2 cache
             wait_vmcnt<0>();
             __syncthreads();
+            // (at most kWholeBefore slots before the window)
             const size_t row = (size_t)(b * A.Hk + hk) * A.cap;
             for (int t = tid; t < first; t += 256) A.a.scores_out[row + t] = A.a.scores[row + t] * A.a.decay;
             const float* kept = A.s + attend_score_at(A, b * A.Hk + hk, 0);

@@ -173,7 +173,9 @@ __global__ void __launch_bounds__(256) k_attend_finish(const AttendArgs A) {
 
 // Up to this many units of 128 tokens a workgroup takes a head alone rather than
 // share it: always up to kWholeUnits, and up to kWholeUnitsMany where the heads
-// alone fill half the chip and two workgroups fit on a compute unit. Microseconds
+// alone fill half the chip and two workgroups fit on a compute unit. By what a
+// sequence's slots, or the window, allow: the host does not know the lengths, so
+// 32 of 1000 in a context of 4096 slots are shared. Microseconds
 // whole and shared, 8 key-value heads of 128: 8 sequences of 250 tokens 8.4 and
 // 11.7, of 500 11.8 and 12.2, of 1000 19.2 and 15.6; 32 of 1000 25.0 and 30.8, on
 // int8 16.3 and 22.4; 160 of up to 1000 on int8 43.8 and 62.1; 80 of 2000 121 and
