@@ -1,9 +1,10 @@
 """Python binding of libdqip.so: the dynamic quantized inner product,
 QuantizeLinear / DequantizeLinear, the requantizing 1x1 QLinearConv, the
 quantized matrix products, the element-wise quantized operators, the
-general QLinearConv, DynamicQuantizeLSTM, and decoding over a paged key-value
-cache (rotary positions, append, attention of one new token, eviction) on AMD
-Instinct MI355X (gfx950).
+general QLinearConv, DynamicQuantizeLSTM, decoding over a paged key-value
+cache (rotary positions, append, attention of one new token, eviction),
+products with 4-bit weights and layers of experts (the same products grouped
+by expert, the router, the sum of the results) on AMD Instinct MI355X (gfx950).
 
 Argument marshalling only: every step runs in the library's HIP kernels.
 The functions carry the names of the C entry points declared in
@@ -30,4 +31,7 @@ from ._binding import (  # noqa: F401
     DQIP_NOALLOC_SCRATCH_BYTES, DQ_ROPE_AXES_MAX, DQ_ROPE_DIM_MAX, dq_rope_forward, dq_rope_info,
     dq_rope_init, dq_rope_release, DQ_KV_BATCH_MAX, DQ_KV_DIM_MAX, dq_kv_append, dq_kv_attend,
     dq_kv_evict, dq_kv_info, dq_kv_init, dq_kv_read, dq_kv_release, dq_kv_take_errors,
+    DQ_MOE_EXPERTS_MAX, DQ_MOE_SIGMOID, DQ_MOE_SOFTMAX, DQ_MOE_TOKENS_MAX, DQ_MOE_TOP_K_MAX, DQ_W4_EXPERTS_MAX,
+    DQ_W4_K_MAX, DQ_W4_N_MAX, DQ_W4_ROWS_MAX, dq_moe_combine, dq_moe_info, dq_moe_init, dq_moe_release, dq_moe_route,
+    dq_w4_forward, dq_w4_forward_grouped, dq_w4_info, dq_w4_init, dq_w4_release, dq_w4_set_w,
 )

@@ -25,6 +25,9 @@ DQ_LSTM_FORWARD, DQ_LSTM_REVERSE, DQ_LSTM_BIDIRECTIONAL = 0, 1, 2
 DQ_LSTM_HIDDEN_MAX = 4096
 DQ_ROPE_DIM_MAX, DQ_ROPE_AXES_MAX = 1024, 8
 DQ_KV_DIM_MAX, DQ_KV_BATCH_MAX = 256, 65535
+DQ_W4_EXPERTS_MAX, DQ_W4_N_MAX, DQ_W4_K_MAX, DQ_W4_ROWS_MAX = 1024, 1 << 20, 1 << 18, 1 << 24
+DQ_MOE_EXPERTS_MAX, DQ_MOE_TOP_K_MAX, DQ_MOE_TOKENS_MAX = 1024, 32, 1 << 24
+DQ_MOE_SOFTMAX, DQ_MOE_SIGMOID = 0, 1
 # dq_rnn_act: ONNX RNN activation name -> (code, takes alpha, default alpha,
 # takes beta, default beta)
 RNN_ACTIVATIONS = {
@@ -117,6 +120,19 @@ _SIGNATURES = {
     "dq_kv_take_errors": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
     "dq_kv_info": (C.c_char_p, [C.c_void_p]),
     "dq_kv_release": (None, [C.c_void_p]),
+    "dq_w4_init": (C.c_int, [C.POINTER(C.c_void_p)] + [C.c_int64] * 4 + [C.c_int] * 4 + [C.c_int64]),
+    "dq_w4_set_w": (C.c_int, [C.c_void_p] * 6),
+    "dq_w4_forward": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
+    "dq_w4_forward_grouped": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
+                                        C.c_void_p, C.c_void_p, C.c_void_p]),
+    "dq_w4_info": (C.c_char_p, [C.c_void_p]),
+    "dq_w4_release": (None, [C.c_void_p]),
+    "dq_moe_init": (C.c_int, [C.POINTER(C.c_void_p), C.c_int64] + [C.c_int] * 5 + [C.c_float]),
+    "dq_moe_route": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64] + [C.c_void_p] * 6),
+    "dq_moe_combine": (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int] + [C.c_void_p] * 3
+                       + [C.c_int, C.c_void_p, C.c_void_p]),
+    "dq_moe_info": (C.c_char_p, [C.c_void_p]),
+    "dq_moe_release": (None, [C.c_void_p]),
     "dq_lstm_info": (C.c_char_p, [C.c_void_p]),
     "dq_lstm_release": (None, [C.c_void_p]),
     "dq_qconv_release": (None, [C.c_void_p]),
@@ -1051,3 +1067,160 @@ def dq_kv_release(ctx):
     _KV_DIMS.pop(ctx, None)
     _KV_TYPES.pop(ctx, None)
     load().dq_kv_release(ctx)
+
+
+# ------------------------------------------------- 4-bit weights and experts
+
+# sizes of each context made by dq_w4_init: (experts, N, K, rows of W, groups,
+# types of x, scales and y)
+_W4_DIMS = {}
+
+
+def dq_w4_init(experts, N, K, group, x_type, scale_type, y_type, gated, max_rows):
+    """Returns the context handle (an int)."""
+    h = C.c_void_p()
+    _check(load().dq_w4_init(C.byref(h), int(experts), int(N), int(K), int(group), x_type, scale_type, y_type,
+                             int(bool(gated)), int(max_rows)), "dq_w4_init")
+    _W4_DIMS[h.value] = (int(experts), int(N), int(K), int(N) * (2 if gated else 1), -(-int(K) // int(group)), x_type,
+                         scale_type, y_type)
+    return h.value
+
+
+def _w4_dims(ctx, what):
+    d = _W4_DIMS.get(ctx)
+    if d is None:
+        raise DQError(DQ_ERR_STATE, what, "no context")
+    return d
+
+
+def dq_w4_set_w(ctx, codes, scales, zeros=None, bias=None, stream=None):
+    """codes: uint8 (or int8: the bytes count) [experts, rows, (K + 1) // 2];
+    scales [experts, rows, G] of the context's type; zeros: uint8 [experts, rows, (G + 1) // 2] or None
+    (every zero point is 8); bias: fp32 [experts, rows] or None."""
+    w = "dq_w4_set_w"
+    e, _, k, rows, g, _, st, _ = _w4_dims(ctx, w)
+    _check(load().dq_w4_set_w(ctx, _dev(codes, w, e * rows * ((k + 1) // 2), DQ_I8),
+                              _dev(scales, w, e * rows * g * _ELEM[st], st),
+                              _dev(zeros, w, e * rows * ((g + 1) // 2), DQ_I8), _dev(bias, w, 4 * e * rows, DQ_F32),
+                              _stream(stream)), w)
+
+
+def _matrix(t, what, cols, type_):
+    """(pointer, rows, row stride) of a [rows, cols] device tensor whose rows
+    are dense."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise DQError(DQ_ERR_ARG, what, f"[rows, {cols}] expected, got {list(shape)}")
+    if not t.is_cuda:
+        raise DQError(DQ_ERR_ARG, what, "not a device tensor")
+    rs, cs = t.stride()
+    if cs != 1 and cols > 1:
+        raise DQError(DQ_ERR_ARG, what, "the last dimension must be dense")
+    if t.dtype is not _TORCH[type_]:
+        _same_type(t, what, type_)
+    return t.data_ptr(), shape[0], rs
+
+
+def dq_w4_forward(ctx, x, y, stream=None):
+    """x [rows, K] (rows may be strided) to y [rows, N], dense."""
+    w = "dq_w4_forward"
+    _, n, k, _, _, xt, _, yt = _w4_dims(ctx, w)
+    xp, rows, stride = _matrix(x, w, k, xt)
+    _check(load().dq_w4_forward(ctx, rows, xp, stride, _dev(y, w, rows * n * _ELEM[yt], yt), _stream(stream)), w)
+
+
+def dq_w4_forward_grouped(ctx, x, offsets, y, row_index=None, stream=None):
+    """y [rows, N], dense: rows offsets[e] to offsets[e + 1] (int32 [experts +
+    1]) are products with expert e's weights, of row row_index[r] (int32
+    [rows]; None: r) of x [x_rows, K] (rows may be strided)."""
+    w = "dq_w4_forward_grouped"
+    e, n, k, _, _, xt, _, yt = _w4_dims(ctx, w)
+    xp, x_rows, stride = _matrix(x, w, k, xt)
+    yp, rows, ys = _matrix(y, w, n, yt)
+    if ys != n and rows > 1:
+        raise DQError(DQ_ERR_ARG, w, "y must be dense")
+    _check(load().dq_w4_forward_grouped(ctx, rows, _dev(offsets, w, 4 * (e + 1), _I32), x_rows, xp, stride,
+                                        _dev(row_index, w, 4 * rows, _I32), yp, _stream(stream)), w)
+
+
+def dq_w4_info(ctx):
+    r = load().dq_w4_info(ctx)
+    return r.decode() if r else None
+
+
+def dq_w4_release(ctx):
+    _W4_DIMS.pop(ctx, None)
+    load().dq_w4_release(ctx)
+
+
+# sizes of each context made by dq_moe_init: (experts, top_k, type of logits)
+_MOE_DIMS = {}
+
+
+def dq_moe_init(max_tokens, experts, top_k, logits_type, scoring=DQ_MOE_SOFTMAX, normalize=True, scale=1.0):
+    """Returns the context handle (an int)."""
+    h = C.c_void_p()
+    _check(load().dq_moe_init(C.byref(h), int(max_tokens), int(experts), int(top_k), logits_type, int(scoring),
+                              int(bool(normalize)), float(scale)), "dq_moe_init")
+    _MOE_DIMS[h.value] = (int(experts), int(top_k), logits_type)
+    return h.value
+
+
+def _moe_dims(ctx, what):
+    d = _MOE_DIMS.get(ctx)
+    if d is None:
+        raise DQError(DQ_ERR_STATE, what, "no context")
+    return d
+
+
+def dq_moe_route(ctx, logits, ids, weights, offsets, row_token, row_of, stream=None):
+    """logits [tokens, experts] (rows may be strided) to ids, row_of (int32)
+    and weights (fp32) [tokens, top_k], offsets int32 [experts + 1] and
+    row_token int32 [tokens * top_k]."""
+    w = "dq_moe_route"
+    e, k, lt = _moe_dims(ctx, w)
+    lp, n, stride = _matrix(logits, w, e, lt)
+    pairs = 4 * n * k
+    _check(load().dq_moe_route(ctx, n, lp, stride, _dev(ids, w, pairs, _I32), _dev(weights, w, pairs, DQ_F32),
+                               _dev(offsets, w, 4 * (e + 1), _I32), _dev(row_token, w, pairs, _I32),
+                               _dev(row_of, w, pairs, _I32), _stream(stream)), w)
+
+
+_FLOATS = {}  # torch dtype -> its code, filled on first use
+
+
+def _float_code(t, what):
+    if not _FLOATS:
+        import torch
+
+        _FLOATS.update({torch.float32: DQ_F32, torch.bfloat16: DQ_BF16, torch.float16: DQ_F16})
+    c = _FLOATS.get(t.dtype)
+    if c is None:
+        raise DQError(DQ_ERR_TYPE, what, f"{t.dtype} is not supported")
+    return c
+
+
+def dq_moe_combine(ctx, y, weights, row_of, out, add=None, stream=None):
+    """out [tokens, N] = add (None: 0) + the sum over j of weights[t, j] (fp32
+    [tokens, top_k]) times row row_of[t, j] (int32) of y [rows, N]; all dense.
+    The types of y and out are their tensors'; add has out's."""
+    w = "dq_moe_combine"
+    _, k, _ = _moe_dims(ctx, w)
+    yt, ot = _float_code(y, w), _float_code(out, w)
+    if len(out.shape) != 2 or len(y.shape) != 2 or y.shape[1] != out.shape[1]:
+        raise DQError(DQ_ERR_ARG, w, f"y [rows, N] and out [tokens, N] expected, got {list(y.shape)}, {list(out.shape)}")
+    n, cols = out.shape
+    rows, size = y.shape[0], n * cols * _ELEM[ot]
+    _check(load().dq_moe_combine(ctx, n, cols, _dev(y, w, rows * cols * _ELEM[yt], yt), rows, yt,
+                                 _dev(weights, w, 4 * n * k, DQ_F32), _dev(row_of, w, 4 * n * k, _I32),
+                                 _dev(add, w, size, ot), ot, _dev(out, w, size, ot), _stream(stream)), w)
+
+
+def dq_moe_info(ctx):
+    r = load().dq_moe_info(ctx)
+    return r.decode() if r else None
+
+
+def dq_moe_release(ctx):
+    _MOE_DIMS.pop(ctx, None)
+    load().dq_moe_release(ctx)

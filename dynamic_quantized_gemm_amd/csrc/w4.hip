@@ -1,0 +1,266 @@
+// w4.hip -- products with 4-bit weights and group scales: contexts, packing
+// and the entry points. The formula and the layout are in w4.h.
+#include "w4.h"
+
+#include <algorithm>
+#include <new>
+#include <stdio.h>
+
+namespace {
+
+using namespace dq;
+
+struct PackArgs {
+    const uint8_t* codes;   // [experts][rows][(K + 1) / 2]
+    const uint8_t* scales;  // [experts][rows][G], 2 or 4 bytes each
+    const uint8_t* zeros;   // [experts][rows][(G + 1) / 2]
+    const float* bias;      // [experts][rows]
+    uint8_t* codes_out;
+    uint8_t* scales_out;
+    uint8_t* zeros_out;
+    float* bias_out;
+    int N, K, group, G, gated, tiles, blocks, S, scale_bytes;
+};
+
+// The caller's row of a packed one, -1 where there is none.
+__device__ __forceinline__ int packed_row(const PackArgs& A, int tile, int c) {
+    if (!A.gated) {
+        const int n = tile * 16 + c;
+        return n < A.N ? n : -1;
+    }
+    const int n = tile / 2 * 16 + c;
+    return n < A.N ? n + (tile & 1) * A.N : -1;
+}
+
+// One workgroup of 64 lanes a block of a tile; grid x: tiles, y: blocks, z: experts.
+__global__ void __launch_bounds__(64) k_w4_pack(PackArgs A) {
+    const int lane = threadIdx.x, tile = blockIdx.x, block = blockIdx.y, e = blockIdx.z;
+    const int rows = A.N * (A.gated ? 2 : 1);
+    const size_t out = ((size_t)e * A.tiles + tile) * A.blocks + block;
+    const int n = packed_row(A, tile, lane & 15), half = (A.K + 1) / 2;
+    u4 w = {0, 0, 0, 0};
+    if (n >= 0) {
+        const uint8_t* row = A.codes + ((size_t)e * rows + n) * half;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            // element i of the caller's order, in byte i / 2, goes to byte i % 4, half i / 4
+            const int k = block * kW4Block + q * 32 + (lane >> 4) * 8;
+            unsigned v = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const unsigned code = k + i < A.K ? (row[(k + i) >> 1] >> (4 * (i & 1))) & 15u : 0u;
+                v |= code << (8 * (i & 3) + 4 * (i >> 2));
+            }
+            w[q] = v;
+        }
+    }
+    reinterpret_cast<u4*>(A.codes_out)[out * 64 + lane] = w;
+    // scales and zero points of 16 rows and S groups
+    if (lane < 16 * A.S) {
+        const int r = packed_row(A, tile, lane / A.S);
+        const int g = (block * kW4Block + lane % A.S * (kW4Block / A.S)) / A.group;
+        const bool some = r >= 0 && g < A.G;
+        const size_t i = some ? ((size_t)e * rows + r) * A.G + g : 0, o = out * 16 * A.S + lane;
+        for (int b = 0; b < A.scale_bytes; ++b)
+            A.scales_out[o * A.scale_bytes + b] = some ? A.scales[i * A.scale_bytes + b] : 0;
+        if (A.zeros_out) {
+            const size_t at = some ? ((size_t)e * rows + r) * ((A.G + 1) / 2) + g / 2 : 0;
+            A.zeros_out[o] = some ? (A.zeros[at] >> (4 * (g & 1))) & 15 : 0;
+        }
+    }
+    if (A.bias_out && block == 0 && lane < 16) {
+        const int r = packed_row(A, tile, lane);
+        A.bias_out[((size_t)e * A.tiles + tile) * 16 + lane] = r >= 0 ? A.bias[(size_t)e * rows + r] : 0.0f;
+    }
+}
+
+int elem_bytes(int type) { return type == DQ_F32 ? 4 : 2; }
+bool is_float(dq_dtype t) { return t == DQ_F32 || t == DQ_BF16 || t == DQ_F16; }
+
+int check_device(const dq_w4_ctx* c) {
+    int dev = 0;
+    (void)hipGetDevice(&dev);
+    if (dev != c->device) DQ_FAIL(DQ_ERR_STATE, "the context belongs to another device");
+    return DQ_OK;
+}
+
+// The tensors of a forward, after its sizes.
+int check_forward(const dq_w4_ctx* c, const void* x, int64_t x_row_stride, const void* y) {
+    if (!c->ready) DQ_FAIL(DQ_ERR_STATE, "no weights: dq_w4_set_w first");
+    if (!x || !y) DQ_FAIL(DQ_ERR_ARG, "x and y must not be NULL");
+    if (x_row_stride < 0) DQ_FAIL(DQ_ERR_ARG, "x_row_stride must be >= 0");
+    if ((uintptr_t)x % elem_bytes(c->x_type) || (uintptr_t)y % elem_bytes(c->y_type))
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    return check_device(c);
+}
+
+W4Args forward_args(const dq_w4_ctx* c, const void* x, int64_t x_row_stride, void* y) {
+    W4Args A{};
+    A.x = x;
+    A.x_stride = x_row_stride;
+    A.codes = c->codes;
+    A.scales = c->scales;
+    A.zeros = c->has_zeros ? c->zeros : nullptr;
+    A.bias = c->has_bias ? c->bias : nullptr;
+    A.y = y;
+    A.N = c->N;
+    A.K = c->K;
+    A.experts = c->experts;
+    A.tiles = c->tiles;
+    A.blocks = c->blocks;
+    A.scale_type = c->scale_type;
+    A.y_type = c->y_type;
+    A.gated = c->gated;
+    // 16 bytes at a time: every row starts at one, and K ends at one
+    const int per16 = 16 / elem_bytes(c->x_type);
+    A.vec = (uintptr_t)x % 16 == 0 && x_row_stride % per16 == 0 && c->K % per16 == 0;
+    return A;
+}
+
+int launch(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
+    // row tiles by the mean rows of an expert: more tiles read the weights once for more rows
+    const int mean = A.offsets ? (A.rows + c->experts - 1) / c->experts : A.rows;
+    const int row_tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4, TM = row_tiles * 16;
+    const int col_tiles = c->gated ? 2 : 1;
+    const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
+    A.col_groups = used / col_tiles;
+    const int64_t tiles_m = A.offsets ? (int64_t)A.rows / TM + std::min(A.rows, c->experts) : (A.rows + TM - 1) / TM;
+    const int64_t grid = tiles_m * A.col_groups;
+    if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
+    int waves = 8;
+    while (waves > 1 && waves / 2 >= c->blocks) waves /= 2;
+    const W4RowsKernel k = c->x_type == DQ_F32    ? w4_rows_f32(row_tiles, col_tiles, c->S)
+                           : c->x_type == DQ_BF16 ? w4_rows_bf16(row_tiles, col_tiles, c->S)
+                                                  : w4_rows_f16(row_tiles, col_tiles, c->S);
+    const size_t lds = (size_t)waves * col_tiles * row_tiles * 1024;
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(waves * 64), lds, s, A);
+    DQ_LAUNCH_CHECK("product with 4-bit weights");
+    return DQ_OK;
+}
+
+}  // namespace
+
+extern "C" int dq_w4_init(dq_w4_ctx** ctx, int64_t experts, int64_t N, int64_t K, int64_t group, dq_dtype x_type,
+                          dq_dtype scale_type, dq_dtype y_type, int gated, int64_t max_rows) {
+    if (!ctx) DQ_FAIL(DQ_ERR_ARG, "ctx is NULL");
+    *ctx = nullptr;
+    if (experts < 1 || N < 1 || K < 1 || max_rows < 1) DQ_FAIL(DQ_ERR_ARG, "sizes must be >= 1");
+    if (group != 32 && group != 64 && (group < 128 || group % 128))
+        DQ_FAIL(DQ_ERR_ARG, "group must be 32, 64 or a multiple of 128");
+    if (!is_float(x_type) || !is_float(scale_type) || !is_float(y_type))
+        DQ_FAIL(DQ_ERR_TYPE, "x, scales and y must be fp32, bf16 or fp16");
+    if (experts > DQ_W4_EXPERTS_MAX || N > DQ_W4_N_MAX || K > DQ_W4_K_MAX || max_rows > DQ_W4_ROWS_MAX)
+        DQ_FAIL(DQ_ERR_RANGE, "experts, N, K or max_rows exceed %d, %d, %d, %d", DQ_W4_EXPERTS_MAX, DQ_W4_N_MAX,
+                DQ_W4_K_MAX, DQ_W4_ROWS_MAX);
+    dq_w4_ctx* c = new (std::nothrow) dq_w4_ctx();
+    if (!c) DQ_FAIL(DQ_ERR_ALLOC, "host allocation for the 4-bit weights' context failed");
+    (void)hipGetDevice(&c->device);
+    if (hipDeviceGetAttribute(&c->cus, hipDeviceAttributeMultiprocessorCount, c->device) != hipSuccess || c->cus < 1)
+        c->cus = 256;
+    c->experts = (int)experts;
+    c->N = (int)N;
+    c->K = (int)K;
+    c->group = (int)std::min<int64_t>(group, 1 << 30);
+    c->x_type = x_type;
+    c->scale_type = scale_type;
+    c->y_type = y_type;
+    c->gated = gated != 0;
+    c->max_rows = max_rows;
+    c->tiles = (int)(((N + 15) / 16 * (gated ? 2 : 1) + kW4TilePad - 1) / kW4TilePad * kW4TilePad);
+    c->blocks = (int)((K + kW4Block - 1) / kW4Block);
+    c->S = group >= 128 ? 1 : (int)(128 / group);
+    const size_t units = (size_t)experts * c->tiles * c->blocks;
+    const bool ok = hipMalloc(&c->codes, units * 1024) == hipSuccess &&
+                    hipMalloc(&c->scales, units * 16 * c->S * elem_bytes(scale_type)) == hipSuccess &&
+                    hipMalloc(&c->zeros, units * 16 * c->S) == hipSuccess &&
+                    hipMalloc(&c->bias, (size_t)experts * c->tiles * 64) == hipSuccess;
+    if (!ok) {
+        dq_w4_release(c);
+        DQ_FAIL(DQ_ERR_ALLOC, "device allocation for the 4-bit weights' context failed");
+    }
+    const char* names[] = {"fp32", "bf16", "int8", "uint8", "fp16"};
+    snprintf(c->info, sizeof c->info, "gfx950 4-bit weights: %d experts, N %d, K %d, groups of %lld, %s x, %s scales, "
+             "%s y%s", c->experts, c->N, c->K, (long long)group, names[x_type], names[scale_type], names[y_type],
+             gated ? ", gated" : "");
+    *ctx = c;
+    return DQ_OK;
+}
+
+extern "C" int dq_w4_set_w(dq_w4_ctx* ctx, const void* codes, const void* scales, const void* zeros, const float* bias,
+                           void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (!codes || !scales) DQ_FAIL(DQ_ERR_ARG, "codes and scales must not be NULL");
+    if ((uintptr_t)scales % elem_bytes(ctx->scale_type) || (uintptr_t)bias % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if (int rc = check_device(ctx)) return rc;
+    PackArgs A{};
+    A.codes = (const uint8_t*)codes;
+    A.scales = (const uint8_t*)scales;
+    A.zeros = (const uint8_t*)zeros;
+    A.bias = bias;
+    A.codes_out = ctx->codes;
+    A.scales_out = (uint8_t*)ctx->scales;
+    A.zeros_out = zeros ? ctx->zeros : nullptr;
+    A.bias_out = bias ? ctx->bias : nullptr;
+    A.N = ctx->N;
+    A.K = ctx->K;
+    A.group = ctx->group;
+    A.G = (ctx->K - 1) / ctx->group + 1;
+    A.gated = ctx->gated;
+    A.tiles = ctx->tiles;
+    A.blocks = ctx->blocks;
+    A.S = ctx->S;
+    A.scale_bytes = elem_bytes(ctx->scale_type);
+    const hipStream_t s = (hipStream_t)stream;
+    ctx->ready = false;
+    hipLaunchKernelGGL(k_w4_pack, dim3(ctx->tiles, ctx->blocks, ctx->experts), dim3(64), 0, s, A);
+    DQ_LAUNCH_CHECK("packing of 4-bit weights");
+    DQ_HIP_CHECK(hipStreamSynchronize(s));
+    ctx->has_zeros = zeros != nullptr;
+    ctx->has_bias = bias != nullptr;
+    ctx->ready = true;
+    return DQ_OK;
+}
+
+extern "C" int dq_w4_forward(dq_w4_ctx* ctx, int64_t rows, const void* x, int64_t x_row_stride, void* y,
+                             void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (ctx->experts != 1) DQ_FAIL(DQ_ERR_ARG, "a context of several experts takes dq_w4_forward_grouped");
+    if (rows < 0 || rows > ctx->max_rows) DQ_FAIL(DQ_ERR_ARG, "rows must lie in [0, %lld]", (long long)ctx->max_rows);
+    if (rows == 0) return DQ_OK;
+    if (int rc = check_forward(ctx, x, x_row_stride, y)) return rc;
+    W4Args A = forward_args(ctx, x, x_row_stride, y);
+    A.rows = A.x_rows = (int)rows;
+    return launch(ctx, A, (hipStream_t)stream);
+}
+
+extern "C" int dq_w4_forward_grouped(dq_w4_ctx* ctx, int64_t rows, const int32_t* offsets, int64_t x_rows,
+                                     const void* x, int64_t x_row_stride, const int32_t* row_index, void* y,
+                                     void* stream) {
+    if (!ctx) DQ_FAIL(DQ_ERR_STATE, "no context");
+    if (rows < 0 || rows > ctx->max_rows) DQ_FAIL(DQ_ERR_ARG, "rows must lie in [0, %lld]", (long long)ctx->max_rows);
+    if (rows == 0) return DQ_OK;
+    if (!offsets) DQ_FAIL(DQ_ERR_ARG, "offsets must not be NULL");
+    if (x_rows < 1 || x_rows > INT32_MAX || (!row_index && x_rows < rows))
+        DQ_FAIL(DQ_ERR_ARG, "x_rows must be >= 1, and cover the rows where there is no row_index");
+    if ((uintptr_t)offsets % 4 || (uintptr_t)row_index % 4)
+        DQ_FAIL(DQ_ERR_ARG, "a tensor is not aligned to its elements");
+    if (int rc = check_forward(ctx, x, x_row_stride, y)) return rc;
+    W4Args A = forward_args(ctx, x, x_row_stride, y);
+    A.rows = (int)rows;
+    A.x_rows = (int)x_rows;
+    A.offsets = offsets;
+    A.row_index = row_index;
+    return launch(ctx, A, (hipStream_t)stream);
+}
+
+extern "C" const char* dq_w4_info(const dq_w4_ctx* ctx) { return ctx ? ctx->info : nullptr; }
+
+extern "C" void dq_w4_release(dq_w4_ctx* ctx) {
+    if (!ctx) return;
+    (void)hipFree(ctx->codes);
+    (void)hipFree(ctx->scales);
+    (void)hipFree(ctx->zeros);
+    (void)hipFree(ctx->bias);
+    delete ctx;
+}

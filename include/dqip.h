@@ -1,8 +1,8 @@
 /*
  * dqip.h -- C ABI of libdqip.so: the dynamic quantized inner product, the
  * QuantizeLinear / DequantizeLinear element-wise operators, the quantized
- * operators around them and decoding over a paged key-value cache on one AMD
- * Instinct MI355X (gfx950).
+ * operators around them, decoding over a paged key-value cache, products with
+ * 4-bit weights and layers of experts on one AMD Instinct MI355X (gfx950).
  *
  * Conventions for every entry point
  *  - Tensor pointers (A, B, C, buf, weight, scale, bias, x, y, scales, zero
@@ -790,6 +790,122 @@ int dq_kv_take_errors(dq_kv_ctx* ctx, int* count, void* stream);
 const char* dq_kv_info(const dq_kv_ctx* ctx);
 /* Frees the context and its device memory; NULL is a no-op. */
 void dq_kv_release(dq_kv_ctx* ctx);
+
+/* ------------------------------------------------------------------------
+ * Products with 4-bit weights and group scales.
+ * Row n of W [rows, K] has a code q (0 to 15) for every k and, for every
+ * `group` values of k, a scale s and a zero point z: W[n, k] = (q - z) s.
+ *   y[m, n] = sum_k x[m, k] W[n, k] + bias[n]
+ * and with gated != 0, where W has 2 N rows (N of a gate, then N of values),
+ *   y[m, n] = silu(v) u,  v = row n's sum, u = row N + n's,
+ *   silu(v) = v / (1 + exp(-v)).
+ * Products are exact and sums fp32, the scale multiplies its group's sum, and
+ * y is rounded once. A NaN or infinity in a row of x gives NaN or infinities in that
+ * row of y and no other; so does one whose sums of code times x leave fp32.
+ *
+ * dq_w4_init: experts matrices of the same sizes (1: dq_w4_forward), each at
+ * most DQ_W4_EXPERTS_MAX, N <= DQ_W4_N_MAX, K <= DQ_W4_K_MAX; group 32, 64 or a
+ * multiple of 128 (one of K or more: one scale a row); the types of x, of the
+ * scales and of y (DQ_F32 / DQ_BF16 / DQ_F16 each); max_rows: the most rows of a
+ * call, <= DQ_W4_ROWS_MAX. Allocates every device buffer of the context (none
+ * later). Errors: DQ_ERR_ARG, DQ_ERR_TYPE, DQ_ERR_RANGE, DQ_ERR_ALLOC,
+ * DQ_ERR_HIP.
+ *
+ * dq_w4_set_w (dense DEVICE tensors): codes [experts, rows, (K + 1) / 2]
+ * bytes, the even k in the low half; scales [experts, rows, G], G = ceil(K /
+ * group); zeros [experts, rows, (G + 1) / 2] bytes, the even group in the low
+ * half (NULL: every z is 8); bias [experts, rows] fp32 (NULL: none). Packs them
+ * into the context and synchronizes `stream`; the caller may free its tensors.
+ * Errors: DQ_ERR_STATE, DQ_ERR_ARG, DQ_ERR_HIP.
+ *
+ * dq_w4_forward (a context of one expert): x has `rows` rows of K elements,
+ * x_row_stride elements apart, y [rows, N] is dense and does not overlap x.
+ * dq_w4_forward_grouped: rows offsets[e] to offsets[e + 1] of y (offsets: int32
+ * [experts + 1] on the device) are products with expert e's weights; row r of
+ * y comes from row row_index[r] (int32 [rows] on the device; NULL: r) of x, which
+ * has x_rows. Rows of y before offsets[0] and from the last offset on are left
+ * as they were. An offset outside [0, rows] counts as the nearest end, one below
+ * the one before it as that one (an expert has no rows then, and rows that two
+ * experts claim get either's); a row_index outside [0, x_rows) gives a row of NaN.
+ * Both are asynchronous on `stream` and allocate nothing; zero rows is a no-op.
+ * Errors: DQ_ERR_STATE (no context or weights, another device), DQ_ERR_ARG,
+ * DQ_ERR_RANGE (beyond one launch), DQ_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+#define DQ_W4_EXPERTS_MAX 1024
+#define DQ_W4_N_MAX (1 << 20)
+#define DQ_W4_K_MAX (1 << 18)
+#define DQ_W4_ROWS_MAX (1 << 24)
+
+typedef struct dq_w4_ctx dq_w4_ctx;
+
+int dq_w4_init(dq_w4_ctx** ctx, int64_t experts, int64_t N, int64_t K, int64_t group, dq_dtype x_type,
+               dq_dtype scale_type, dq_dtype y_type, int gated, int64_t max_rows);
+int dq_w4_set_w(dq_w4_ctx* ctx, const void* codes, const void* scales, const void* zeros, const float* bias,
+                void* stream);
+int dq_w4_forward(dq_w4_ctx* ctx, int64_t rows, const void* x, int64_t x_row_stride, void* y, void* stream);
+int dq_w4_forward_grouped(dq_w4_ctx* ctx, int64_t rows, const int32_t* offsets, int64_t x_rows, const void* x,
+                          int64_t x_row_stride, const int32_t* row_index, void* y, void* stream);
+/* A short description of the context (owned by it); NULL for NULL. */
+const char* dq_w4_info(const dq_w4_ctx* ctx);
+/* Frees the context and its device memory; NULL is a no-op. */
+void dq_w4_release(dq_w4_ctx* ctx);
+
+/* ------------------------------------------------------------------------
+ * Layers of experts: the router, and the sum of the experts' results.
+ *
+ * dq_moe_init: at most max_tokens (<= DQ_MOE_TOKENS_MAX) tokens a call, experts
+ * <= DQ_MOE_EXPERTS_MAX, top_k <= experts and DQ_MOE_TOP_K_MAX, the logits' type
+ * (DQ_F32 / DQ_BF16 / DQ_F16), scoring, normalize, and a finite factor `scale` of
+ * all weights. Allocates every device buffer of the context (none later).
+ * Errors: DQ_ERR_ARG, DQ_ERR_TYPE, DQ_ERR_RANGE, DQ_ERR_ALLOC, DQ_ERR_HIP.
+ *
+ * dq_moe_route: logits (token t's at t * logits_stride, `experts` of them; DEVICE)
+ * to, all dense on the device:
+ *   ids [tokens, top_k] int32   the experts of the top_k largest logits in
+ *     falling order, equal ones by the lowest expert; one at -infinity or NaN is never
+ *     chosen, and where too few are left the places hold -1
+ *   weights [tokens, top_k] fp32   DQ_MOE_SOFTMAX: exp(l) over the sum of all
+ *     experts' exp(l); DQ_MOE_SIGMOID: 1 / (1 + exp(-l)); with normalize over the
+ *     sum of the chosen ones; times scale; 0 where the id is -1. With softmax a NaN
+ *     or +infinity among a token's logits gives it NaN weights
+ *   offsets [experts + 1] int32, row_token and row_of: the pairs (t, j) with an
+ *     expert, ordered by the expert and then the token, are rows 0 to
+ *     offsets[experts]; those of expert e begin at offsets[e], row_token[row] int32
+ *     [tokens * top_k] is a row's token (entries from the last row on are left as
+ *     they were), row_of [tokens, top_k] int32 a pair's row, -1 where the id is -1.
+ * offsets and row_token are what dq_w4_forward_grouped takes. Zero tokens writes
+ * offsets of zeros.
+ *
+ * dq_moe_combine: out[t] = add[t] + sum_j weights[t, j] y[row_of[t, j]] for y
+ * [rows, N], out and add (NULL: 0) [tokens, N], dense (DEVICE; y_type, out_type:
+ * DQ_F32 / DQ_BF16 / DQ_F16; add has out's type and may be out), summed in fp32
+ * in the order of j and rounded once. A row_of below 0 adds nothing whatever its
+ * weight, one of rows or more gives NaN. It needs no workspace: calls may overlap.
+ *
+ * Both are asynchronous on `stream` and allocate nothing. dq_moe_route uses the
+ * context's workspace: its calls on one context must not overlap. Errors:
+ * DQ_ERR_STATE (no context, another device), DQ_ERR_ARG, DQ_ERR_TYPE, DQ_ERR_RANGE
+ * (beyond one launch), DQ_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+#define DQ_MOE_EXPERTS_MAX 1024
+#define DQ_MOE_TOP_K_MAX 32
+#define DQ_MOE_TOKENS_MAX (1 << 24)
+
+typedef enum DQ_ENUM_INT { DQ_MOE_SOFTMAX = 0, DQ_MOE_SIGMOID = 1 } dq_moe_scoring;
+
+typedef struct dq_moe_ctx dq_moe_ctx;
+
+int dq_moe_init(dq_moe_ctx** ctx, int64_t max_tokens, int experts, int top_k, dq_dtype logits_type, int scoring,
+                int normalize, float scale);
+int dq_moe_route(dq_moe_ctx* ctx, int64_t tokens, const void* logits, int64_t logits_stride, int32_t* ids,
+                 float* weights, int32_t* offsets, int32_t* row_token, int32_t* row_of, void* stream);
+int dq_moe_combine(dq_moe_ctx* ctx, int64_t tokens, int64_t N, const void* y, int64_t rows, dq_dtype y_type,
+                   const float* weights, const int32_t* row_of, const void* add, dq_dtype out_type, void* out,
+                   void* stream);
+/* A short description of the context (owned by it); NULL for NULL. */
+const char* dq_moe_info(const dq_moe_ctx* ctx);
+/* Frees the context and its device memory; NULL is a no-op. */
+void dq_moe_release(dq_moe_ctx* ctx);
 
 #ifdef __cplusplus
 }
