@@ -63,16 +63,28 @@ struct dq_w4_ctx {
     void* scales = nullptr;
     uint8_t* zeros = nullptr;
     float* bias = nullptr;
+    // many rows: sums of x's groups and rows prepared for sums_rows and copy_rows
+    // rows at a time (0: the context takes few rows)
+    float* sums = nullptr;
+    uint16_t* copy = nullptr;
+    int64_t sums_rows = 0, copy_rows = 0;
     char info[192] = "";
 };
 
+// What the files of each type of x offer: the kernel for few rows (w4_rows.h)
+// by row and column tiles of 16 a workgroup, the kernel for many (w4_tile.h) by
+// the workgroup's columns / 64, and the latter's preparation; S as above.
 namespace dq {
 
-// Launches of the kernel for few rows (w4_rows.h), one for each type of x:
-// waves a workgroup, row tiles of 16 and column tiles a workgroup, S.
-typedef void (*W4RowsKernel)(W4Args);
-W4RowsKernel w4_rows_bf16(int row_tiles, int col_tiles, int S);
-W4RowsKernel w4_rows_f16(int row_tiles, int col_tiles, int S);
-W4RowsKernel w4_rows_f32(int row_tiles, int col_tiles, int S);
+struct W4TileArgs;
+struct W4Prepare;
+struct W4Kernels {
+    void (*(*rows)(int row_tiles, int col_tiles, int S))(W4Args);
+    void (*(*tile)(int wide, int S))(W4TileArgs);
+    void (*prepare)(W4Prepare);
+};
+W4Kernels w4_kernels_bf16();
+W4Kernels w4_kernels_f16();
+W4Kernels w4_kernels_f32();
 
 }  // namespace dq

@@ -1,6 +1,6 @@
 // w4.hip -- products with 4-bit weights and group scales: contexts, packing
 // and the entry points. The formula and the layout are in w4.h.
-#include "w4.h"
+#include "w4_tile.h"
 
 #include <algorithm>
 #include <new>
@@ -9,6 +9,11 @@
 namespace {
 
 using namespace dq;
+
+// rows an expert from which the kernel for many rows is taken
+constexpr int kTileMean = 64;
+// bytes that a context keeps for prepared rows; more rows go in several launches
+constexpr int64_t kCopyBytes = 64 << 20, kSumsBytes = 32 << 20;
 
 struct PackArgs {
     const uint8_t* codes;   // [experts][rows][(K + 1) / 2]
@@ -117,7 +122,11 @@ W4Args forward_args(const dq_w4_ctx* c, const void* x, int64_t x_row_stride, voi
     return A;
 }
 
-int launch(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
+W4Kernels kernels_of(const dq_w4_ctx* c) {
+    return c->x_type == DQ_F32 ? w4_kernels_f32() : c->x_type == DQ_BF16 ? w4_kernels_bf16() : w4_kernels_f16();
+}
+
+int launch_rows(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
     // row tiles by the mean rows of an expert: more tiles read the weights once for more rows
     const int mean = A.offsets ? (A.rows + c->experts - 1) / c->experts : A.rows;
     const int row_tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4, TM = row_tiles * 16;
@@ -129,13 +138,85 @@ int launch(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
     if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
     int waves = 8;
     while (waves > 1 && waves / 2 >= c->blocks) waves /= 2;
-    const W4RowsKernel k = c->x_type == DQ_F32    ? w4_rows_f32(row_tiles, col_tiles, c->S)
-                           : c->x_type == DQ_BF16 ? w4_rows_bf16(row_tiles, col_tiles, c->S)
-                                                  : w4_rows_f16(row_tiles, col_tiles, c->S);
     const size_t lds = (size_t)waves * col_tiles * row_tiles * 1024;
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(waves * 64), lds, s, A);
+    hipLaunchKernelGGL(kernels_of(c).rows(row_tiles, col_tiles, c->S), dim3((unsigned)grid), dim3(waves * 64), lds, s, A);
     DQ_LAUNCH_CHECK("product with 4-bit weights");
     return DQ_OK;
+}
+
+// The tile kernel's offsets within x are 32 bits.
+bool tile_reaches(const dq_w4_ctx* c, const W4Args& A) {
+    const __int128 rows = A.row_index ? A.x_rows : kW4TileRows;
+    return rows * A.x_stride * 2 + A.K * 2 < ((__int128)1 << 32);
+}
+
+int launch_tile(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
+    const W4Kernels k = kernels_of(c);
+    // rows of whole blocks of 16 bits that lie 16 bytes apart are taken where they are
+    const bool copy = c->x_type == DQ_F32 || !A.vec || c->K % kW4Block || !tile_reaches(c, A);
+    const int64_t slab = copy ? c->copy_rows : c->sums_rows;
+    // rows of x are prepared once where they all fit, else as rows of y
+    const bool by_row = A.row_index ? A.x_rows > slab || A.x_rows > A.rows : true;
+    const int P = c->x_type == DQ_F32 ? 3 : 1, Kp = c->blocks * kW4Block;
+    for (int64_t lo = 0; lo < A.rows; lo += slab) {
+        const int64_t hi = std::min<int64_t>(A.rows, lo + slab);
+        if (by_row || lo == 0) {
+            W4Prepare B{};
+            B.x = A.x;
+            B.x_stride = A.x_stride;
+            B.rows = by_row ? (int)(hi - lo) : A.x_rows;
+            B.x_rows = A.x_rows;
+            if (by_row && A.row_index) B.row_index = A.row_index + lo;
+            else if (by_row) {
+                B.x = (const char*)A.x + lo * A.x_stride * elem_bytes(c->x_type);
+                B.x_rows = B.rows;
+            }
+            B.K = c->K;
+            B.blocks = c->blocks;
+            B.S = c->S;
+            B.vec = A.vec;
+            B.copy = copy ? c->copy : nullptr;
+            B.sums = c->sums;
+            hipLaunchKernelGGL(k.prepare, dim3((unsigned)((B.rows + 3) / 4)), dim3(256), 0, s, B);
+            DQ_LAUNCH_CHECK("preparation of rows");
+        }
+        W4TileArgs T{};
+        T.a = A;
+        T.sums = c->sums;
+        T.by_row = by_row;
+        T.x_by_row = by_row && copy;
+        if (copy) {
+            T.a.x = c->copy;
+            T.a.x_stride = (long long)P * Kp;
+        }
+        T.row_lo = (int)lo;
+        T.row_hi = (int)hi;
+        const int wide = 2;
+        const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
+        T.tiles_n = (used + 4 * wide - 1) / (4 * wide);
+        const int64_t rows = hi - lo;
+        const int64_t tiles_m = A.offsets ? rows / kW4TileRows + std::min<int64_t>(rows, c->experts)
+                                          : (rows + kW4TileRows - 1) / kW4TileRows;
+        T.tiles_m = (int)tiles_m;
+        // units of 4 x 8 tiles to an XCD, smaller ones where there are few
+        T.gm = 4;
+        T.gn = 8;
+        auto units = [&] { return (tiles_m + T.gm - 1) / T.gm * ((T.tiles_n + T.gn - 1) / T.gn); };
+        while (T.gn > 1 && units() < 32) T.gn /= 2;
+        while (T.gm > 1 && units() < 32) T.gm /= 2;
+        const int64_t grid = (units() + 7) / 8 * 8 * T.gm * T.gn;
+        if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
+        T.vec_store = (uintptr_t)A.y % 16 == 0 && c->N % 8 == 0;
+        hipLaunchKernelGGL(k.tile(wide, c->S), dim3((unsigned)grid), dim3(128 * wide), 0, s, T);
+        DQ_LAUNCH_CHECK("product with 4-bit weights");
+    }
+    return DQ_OK;
+}
+
+int launch(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
+    const int mean = A.offsets ? (A.rows + c->experts - 1) / c->experts : A.rows;
+    if (mean > kTileMean && c->copy_rows) return launch_tile(c, A, s);
+    return launch_rows(c, A, s);
 }
 
 }  // namespace
@@ -170,6 +251,18 @@ extern "C" int dq_w4_init(dq_w4_ctx** ctx, int64_t experts, int64_t N, int64_t K
     c->blocks = (int)((K + kW4Block - 1) / kW4Block);
     c->S = group >= 128 ? 1 : (int)(128 / group);
     const size_t units = (size_t)experts * c->tiles * c->blocks;
+    if (max_rows > kTileMean) {
+        const int64_t row = (int64_t)c->blocks * kW4Block * 2 * (x_type == DQ_F32 ? 3 : 1), sum = (int64_t)c->blocks * c->S * 4;
+        auto fit = [&](int64_t bytes, int64_t one) {
+            return std::min(max_rows, std::max<int64_t>(kW4TileRows, bytes / one / kW4TileRows * kW4TileRows));
+        };
+        c->copy_rows = fit(kCopyBytes, row);
+        c->sums_rows = std::max(c->copy_rows, fit(kSumsBytes, sum));
+        if (hipMalloc(&c->copy, c->copy_rows * row) != hipSuccess || hipMalloc(&c->sums, c->sums_rows * sum) != hipSuccess) {
+            dq_w4_release(c);
+            DQ_FAIL(DQ_ERR_ALLOC, "device allocation for the 4-bit weights' context failed");
+        }
+    }
     const bool ok = hipMalloc(&c->codes, units * 1024) == hipSuccess &&
                     hipMalloc(&c->scales, units * 16 * c->S * elem_bytes(scale_type)) == hipSuccess &&
                     hipMalloc(&c->zeros, units * 16 * c->S) == hipSuccess &&
@@ -262,5 +355,7 @@ extern "C" void dq_w4_release(dq_w4_ctx* ctx) {
     (void)hipFree(ctx->scales);
     (void)hipFree(ctx->zeros);
     (void)hipFree(ctx->bias);
+    (void)hipFree(ctx->sums);
+    (void)hipFree(ctx->copy);
     delete ctx;
 }

@@ -1,8 +1,9 @@
 // w4_bf16.hip -- the 4-bit weights' kernels for bf16 rows of x.
 #include "w4_rows.h"
+#include "w4_tile.h"
 
 namespace dq {
 
-W4RowsKernel w4_rows_bf16(int row_tiles, int col_tiles, int S) { return w4_rows_pick<DQ_BF16>(row_tiles, col_tiles, S); }
+W4Kernels w4_kernels_bf16() { return {w4_rows_pick<DQ_BF16>, w4_tile_pick<DQ_BF16>, k_w4_prepare<DQ_BF16>}; }
 
 }  // namespace dq

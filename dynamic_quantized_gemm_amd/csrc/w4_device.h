@@ -46,6 +46,7 @@ struct W4Op<DQ_BF16> {
                       __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true))};
         return r;
     }
+    static __device__ __forceinline__ float value(unsigned b) { return bf16_bits_to_f32(b); }
     static __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
     }
@@ -65,6 +66,9 @@ struct W4Op<DQ_F16> {
                       __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false)),
                       __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true))};
         return r;
+    }
+    static __device__ __forceinline__ float value(unsigned b) {
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)b);
     }
     static __device__ __forceinline__ f4 mfma(u4 a, u4 b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
@@ -119,25 +123,54 @@ __device__ __forceinline__ void w4_store(void* y, size_t i, float v, int type) {
     else static_cast<_Float16*>(y)[i] = (_Float16)v;
 }
 
+// Eight neighbouring elements of a row of y, from column n on; those from N on
+// are not stored. vec: every row and n is 16-byte aligned.
+__device__ __forceinline__ void w4_store8(void* y, size_t row, int n, int N, const float* v, int type, bool vec) {
+    if (vec && n + 8 <= N) {
+        const f4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+        if (type == DQ_F32) {
+            f4* p = reinterpret_cast<f4*>(static_cast<float*>(y) + row + n);
+            p[0] = lo;
+            p[1] = hi;
+            return;
+        }
+        u4 w;
+        if (type == DQ_BF16) {
+            const u2 l = f32x4_to_bf16x4(lo), h = f32x4_to_bf16x4(hi);
+            w = u4{l[0], l[1], h[0], h[1]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const h2 p = {(_Float16)v[2 * i], (_Float16)v[2 * i + 1]};
+                w[i] = __builtin_bit_cast(unsigned, p);
+            }
+        }
+        *reinterpret_cast<u4*>(static_cast<uint16_t*>(y) + row + n) = w;
+        return;
+    }
+    for (int i = 0; i < 8; ++i)
+        if (n + i < N) w4_store(y, row + n + i, v[i], type);
+}
+
 __device__ __forceinline__ float w4_silu(float v) { return v / (1.0f + expf(-v)); }
 
 // The rows of the t-th row tile of TM rows: expert, first row, end. Without
 // offsets there is one expert. Offsets that do not increase or leave
-// [0, rows] are taken as the nearest that do. Every wave finds its tile by
+// [lo, hi] are taken as the nearest that do. Every wave finds its tile by
 // itself: 64 experts at a time, a prefix sum of their tiles.
 struct W4Tile {
     int expert, first, end;  // first == end: no such tile
 };
-__device__ __forceinline__ W4Tile w4_tile(const W4Args& A, int t, int TM) {
-    if (!A.offsets) return {0, min(t * TM, A.rows), min(A.rows, t * TM + TM)};
+__device__ __forceinline__ W4Tile w4_tile(const W4Args& A, int t, int TM, int lo, int hi) {
+    if (!A.offsets) return {0, min(lo + t * TM, hi), min(hi, lo + t * TM + TM)};
     const int lane = threadIdx.x & 63;
     int before = 0;
     for (int e0 = 0; e0 < A.experts; e0 += 64) {
         const int e = e0 + lane;
         int a = 0, b = 0;
         if (e < A.experts) {
-            a = min(max(A.offsets[e], 0), A.rows);
-            b = min(max(A.offsets[e + 1], a), A.rows);
+            a = min(max(A.offsets[e], lo), hi);
+            b = min(max(A.offsets[e + 1], a), hi);
         }
         const int n = (b - a + TM - 1) / TM;
         int upto = n;

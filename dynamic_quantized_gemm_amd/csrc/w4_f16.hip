@@ -1,8 +1,9 @@
 // w4_f16.hip -- the 4-bit weights' kernels for fp16 rows of x.
 #include "w4_rows.h"
+#include "w4_tile.h"
 
 namespace dq {
 
-W4RowsKernel w4_rows_f16(int row_tiles, int col_tiles, int S) { return w4_rows_pick<DQ_F16>(row_tiles, col_tiles, S); }
+W4Kernels w4_kernels_f16() { return {w4_rows_pick<DQ_F16>, w4_tile_pick<DQ_F16>, k_w4_prepare<DQ_F16>}; }
 
 }  // namespace dq

@@ -1,8 +1,9 @@
 // w4_f32.hip -- the 4-bit weights' kernels for fp32 rows of x.
 #include "w4_rows.h"
+#include "w4_tile.h"
 
 namespace dq {
 
-W4RowsKernel w4_rows_f32(int row_tiles, int col_tiles, int S) { return w4_rows_pick<DQ_F32>(row_tiles, col_tiles, S); }
+W4Kernels w4_kernels_f32() { return {w4_rows_pick<DQ_F32>, w4_tile_pick<DQ_F32>, k_w4_prepare<DQ_F32>}; }
 
 }  // namespace dq

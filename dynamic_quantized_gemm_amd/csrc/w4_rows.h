@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kW4RowsWaves * 64) k_w4_rows(W4Args A) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int c = lane & 15, quad = lane >> 4;
     const int group = blockIdx.x % A.col_groups;
-    const W4Tile tile = w4_tile(A, blockIdx.x / A.col_groups, TM);
+    const W4Tile tile = w4_tile(A, blockIdx.x / A.col_groups, TM, 0, A.rows);
     if (tile.first >= tile.end) return;
     const int t0 = group * CT;
 
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kW4RowsWaves * 64) k_w4_rows(W4Args A) {
 }
 
 // the instances for one type of x
+typedef void (*W4RowsKernel)(W4Args);
 template <int T, int RT, int CT>
 W4RowsKernel w4_rows_pick(int S) {
     return S == 4 ? k_w4_rows<T, RT, CT, 4> : S == 2 ? k_w4_rows<T, RT, CT, 2> : k_w4_rows<T, RT, CT, 1>;

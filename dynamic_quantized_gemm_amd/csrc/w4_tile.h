@@ -1,0 +1,347 @@
+// w4_tile.h -- the kernel of products with 4-bit weights for many rows.
+//
+// Bound by the matrix cores. A workgroup of 2 x WN waves computes 128 rows by
+// 64 WN columns of the packed order, a wave 64 x 64 of them (4 x 4 blocks of
+// 16 x 16). K advances by a block of 128: the rows of x come straight to LDS
+// (two stages, 32 KiB each, the next one on its way while this one is
+// multiplied), swizzled so that the 16 rows of an operand lie in different
+// banks; the codes come straight to registers, one 1 KiB load for 16 columns, and are
+// unpacked there.
+//
+// The scale of a group multiplies its sum: sums start anew with every group
+// and are added to the result with one fused multiply-add each, as many
+// vector operations for 4 matrix operations of a group of 128 as their issue
+// leaves time for. A group's sum starts at -8 times the group's sum of x, which
+// takes the middle of the codes out at no cost (the operand is there anyway);
+// the rest of a zero point, z - 8, is one small product over the groups
+// at the end, in three bf16 pieces of each side (24 bits). The sums of x come from
+// k_w4_prepare, which also makes aligned rows of what is not: K padded to whole
+// blocks, fp32 as three bf16 pieces one behind the other.
+#pragma once
+
+#include "w4_device.h"
+
+#include <type_traits>
+
+namespace dq {
+
+constexpr int kW4TileRows = 128;
+
+// Rows of x as the tile kernel takes them, and the sums of their groups.
+struct W4Prepare {
+    const void* x;
+    long long x_stride;
+    const int32_t* row_index;  // row r is x's row_index[r] (NULL: r)
+    int rows, x_rows, K, blocks, S, vec;
+    uint16_t* copy;  // [rows][P][blocks * 128] (NULL: sums only)
+    float* sums;     // [rows][blocks * S]: -8 times a group's sum
+};
+
+// A wave a row; each lane takes 8 elements of a block's 128, four blocks at a time.
+template <int T>
+__global__ void __launch_bounds__(256) k_w4_prepare(W4Prepare A) {
+    using O = W4Op<T>;
+    constexpr int P = O::P;
+    const int lane = threadIdx.x & 63;
+    const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r >= A.rows) return;
+    long long src = A.row_index ? A.row_index[r] : r;
+    if (src < 0 || src >= A.x_rows) src = 0;  // its results are NaN in any case
+    const char* row = static_cast<const char*>(A.x) + src * A.x_stride * O::elem;
+    const int Kp = A.blocks * kW4Block;
+    for (int b = lane >> 4; b < A.blocks; b += 4) {
+        const int k = b * kW4Block + (lane & 15) * 8;
+        u4 x[P];
+        w4_load8<T>(row, k, A.K, A.vec, x);
+        if (A.copy)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<u4*>(A.copy + ((size_t)r * P + p) * Kp + k) = x[p];
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = 0.0f;
+#pragma unroll
+                for (int p = P - 1; p >= 0; --p) v += O::value((x[p][i] >> (16 * h)) & 0xffffu);
+                s += v;
+            }
+        // the 16 lanes of a block hold 16, 8 or 4 lanes of a group
+        s += __shfl_xor(s, 1);
+        s += __shfl_xor(s, 2);
+        if (A.S <= 2) s += __shfl_xor(s, 4);
+        if (A.S == 1) s += __shfl_xor(s, 8);
+        const int per = 16 / A.S;
+        if ((lane & (per - 1)) == 0) A.sums[(size_t)r * A.blocks * A.S + b * A.S + (lane & 15) / per] = -8.0f * s;
+    }
+}
+
+struct W4TileArgs {
+    W4Args a;           // x: rows of P * blocks * 128 elements
+    const float* sums;  // by the row of x, or of y from row_lo on where by_row
+    int by_row;
+    int x_by_row;       // and so are the rows of a.x
+    int row_lo, row_hi; // the rows of y that this launch takes
+    int tiles_m, tiles_n, gm, gn;  // the most tiles; gm x gn neighbours go to one XCD
+    int vec_store;
+};
+
+template <int T, int WN, int S>
+__global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
+    using O = W4Op<T>;
+    constexpr int P = O::P, NW = 2 * WN, CPW = 32 / NW;  // waves, copies a wave and stage
+    __shared__ __attribute__((aligned(16))) char st0[kW4TileRows * 256];
+    __shared__ __attribute__((aligned(16))) char st1[kW4TileRows * 256];
+    __shared__ __attribute__((aligned(16))) float s_sum[2][S][kW4TileRows];
+    __shared__ int s_bad[kW4TileRows];
+    const W4Args& a = A.a;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, quad = lane >> 4;
+    const int wm = wave / WN, wn = wave % WN;
+
+    // Neighbouring workgroups land on different XCDs (round robin): each XCD
+    // takes whole units of gm x gn tiles, which share x and codes in its L2.
+    const int per = A.gm * A.gn, xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+    const int unit = (j / per) * 8 + xcd, in = j % per;
+    const int units_n = (A.tiles_n + A.gn - 1) / A.gn;
+    const int tm = unit / units_n * A.gm + in % A.gm, tn = unit % units_n * A.gn + in / A.gm;
+    if (tm >= A.tiles_m || tn >= A.tiles_n) return;
+    const W4Tile tile = w4_tile(a, tm, kW4TileRows, A.row_lo, A.row_hi);
+    if (tile.first >= tile.end) return;
+
+    // Copies of x: each takes 4 rows of 256 bytes, lane l the 16-byte piece (l %
+    // 16) ^ (row % 16) of row l / 16, to LDS in the order of the lanes.
+    const int last = tile.end - 1;
+    uint32_t voff[CPW];
+    const bool gather = a.row_index && !A.x_by_row;
+    const long long row0 = gather ? 0 : tile.first - (A.x_by_row ? A.row_lo : 0);
+    const char* xbase = static_cast<const char*>(a.x) + row0 * a.x_stride * 2;
+#pragma unroll
+    for (int i = 0; i < CPW; ++i) {
+        const int r = (wave * CPW + i) * 4 + quad, at = min(tile.first + r, last);
+        int src = a.row_index ? a.row_index[at] : 0;
+        const bool bad = a.row_index && (src < 0 || src >= a.x_rows);
+        if (c == 0) s_bad[r] = bad;
+        if (!gather) src = at - tile.first;
+        else if (bad) src = 0;
+        voff[i] = (uint32_t)((long long)src * a.x_stride * 2) + (uint32_t)((c ^ (r & 15)) * 16);
+    }
+    auto copy = [&](int stage_k, char* dst) {
+        // stage_k: the element of a row at which the stage's 128 begin
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) copy16_to_lds(xbase + (size_t)stage_k * 2 + voff[i], dst + (wave * CPW + i) * 1024);
+    };
+    // the sums of x of thread t's row (t < 128)
+    const float* sum_row;
+    {
+        const int r = min(tile.first + (int)(threadIdx.x & (kW4TileRows - 1)), last);
+        int src = r;
+        if (A.by_row) src = r - A.row_lo;
+        else if (a.row_index) {
+            src = a.row_index[r];
+            if (src < 0 || src >= a.x_rows) src = 0;
+        }
+        sum_row = A.sums + (size_t)src * a.blocks * S;
+    }
+    const int nt0 = tn * (WN * 4) + wn * 4;  // this wave's column tiles
+    const size_t base = (size_t)tile.expert * a.tiles + nt0;
+    const u4* codes = reinterpret_cast<const u4*>(a.codes) + base * a.blocks * 64 + lane;
+    const size_t code_step = (size_t)a.blocks * 64;
+
+    f4 acc[4][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) acc[m][n] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    u4 code[2][4];
+    float sc[2][4][S], sum[S];
+    const int nstages = a.blocks * P, Kp = a.blocks * kW4Block;
+
+    auto fetch = [&](int b, u4* w, float (*s)[S]) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) w[n] = codes[n * code_step + (size_t)b * 64];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int g = 0; g < S; ++g)
+                s[n][g] = w4_scale(a.scales, (((base + n) * a.blocks + b) * 16 + c) * S + g, a.scale_type);
+    };
+    auto fetch_sums = [&](int b) {
+#pragma unroll
+        for (int g = 0; g < S; ++g) sum[g] = sum_row[b * S + g];
+    };
+
+    copy(0, st0);
+    fetch(0, code[0], sc[0]);
+    if (threadIdx.x < kW4TileRows) fetch_sums(0);
+
+    auto stage = [&](auto CUR, int i) {
+        constexpr int cur = decltype(CUR)::value;
+        const char* L = cur ? st1 : st0;
+        if (threadIdx.x < kW4TileRows)
+#pragma unroll
+            for (int g = 0; g < S; ++g) s_sum[cur][g][threadIdx.x] = sum[g];
+        wait_vmcnt_lgkm0<0>();
+        lds_barrier();
+        // past the end the last stage again: in bounds, not used
+        const int nx = min(i + 1, nstages - 1), nb = P == 1 ? nx : nx / P;
+        copy(nb * kW4Block + (nx - nb * P) * Kp, cur ? st0 : st1);
+        fetch(nb, code[cur ^ 1], sc[cur ^ 1]);
+        if (threadIdx.x < kW4TileRows) fetch_sums(nb);
+        const bool first = P == 1 || i % P == 0;
+#pragma unroll
+        for (int g = 0; g < S; ++g) {
+            f4 t[4][4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                f4 t0 = *reinterpret_cast<const f4*>(&s_sum[cur][g][wm * 64 + m * 16 + quad * 4]);
+                if (!first) t0 = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) t[m][n] = t0;
+            }
+#pragma unroll
+            for (int q = g * (4 / S); q < (g + 1) * (4 / S); ++q) {
+                u4 x[4], w[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int r = wm * 64 + m * 16 + c;
+                    x[m] = *reinterpret_cast<const u4*>(L + r * 256 + (((q * 4 + quad) ^ c) * 16));
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) w[n] = O::codes(code[cur][n][q]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) t[m][n] = O::mfma(x[m], w[n], t[m][n]);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(sc[cur][n][g], t[m][n][v], acc[m][n][v]);
+            if (g + 1 < S) __builtin_amdgcn_sched_barrier(0);  // one group's sums in registers at a time
+        }
+    };
+    int i = 0;
+    for (; i + 2 <= nstages; i += 2) {
+        stage(std::integral_constant<int, 0>{}, i);
+        stage(std::integral_constant<int, 1>{}, i + 1);
+    }
+    if (i < nstages) stage(std::integral_constant<int, 0>{}, i);
+    wait_vmcnt_lgkm0<0>();
+    lds_barrier();  // nobody reads a stage any more, nothing is on its way to one
+
+    // what is left of the zero points: (z - 8) s of 32 groups at a time against
+    // the sums of x, which are there times -8
+    if (a.zeros) {
+        const int groups = a.blocks * S;
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            u4 zs[4][3];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int g = min(g0 + quad * 8 + k, groups - 1), b = g / S;
+                    const size_t at = (((base + n) * a.blocks + b) * 16 + c) * S + g % S;
+                    v[k] = g0 + quad * 8 + k < groups
+                               ? w4_scale(a.scales, at, a.scale_type) * (((float)a.zeros[at] - 8.0f) * 0.125f)
+                               : 0.0f;
+                }
+                split3(v, &zs[n][0], &zs[n][1], &zs[n][2]);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int r = min(tile.first + wm * 64 + m * 16 + c, last);
+                int src = A.by_row ? r - A.row_lo : r;
+                if (!A.by_row && a.row_index) {
+                    src = a.row_index[r];
+                    if (src < 0 || src >= a.x_rows) src = 0;
+                }
+                const float* p = A.sums + (size_t)src * groups;
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int g = g0 + quad * 8 + k;
+                    v[k] = g < groups ? p[min(g, groups - 1)] : 0.0f;
+                }
+                u4 xs[3];
+                split3(v, &xs[0], &xs[1], &xs[2]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int u = 0; u < 3; ++u)
+#pragma unroll
+                        for (int w = 0; u + w < 3; ++w)
+                            acc[m][n] = W4Op<DQ_BF16>::mfma(xs[u], zs[n][w], acc[m][n]);
+            }
+        }
+    }
+
+    // bias and gate, through this wave's part of the stages (32 rows at a time)
+    // so that whole rows go out, 16 bytes a lane
+    constexpr int kPart = 2 * kW4TileRows * 256 / NW;  // 16 KiB or 8
+    constexpr int kRows = kPart / 256 < 64 ? kPart / 256 : 64;
+    char* part_base = wave < NW / 2 ? st0 + wave * kPart : st1 + (wave - NW / 2) * kPart;
+    float* part = reinterpret_cast<float*>(part_base);
+    const int cols = a.gated ? 32 : 64;
+    const int n0 = (a.gated ? nt0 / 2 : nt0) * 16;
+    if (a.bias)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float bias = a.bias[(base + n) * 16 + c];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[m][n][v] += bias;
+        }
+#pragma unroll
+    for (int p0 = 0; p0 < 64; p0 += kRows) {
+#pragma unroll
+        for (int m = 0; m < kRows / 16; ++m)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                f4 v = acc[p0 / 16 + m][n];
+                int col = n * 16;
+                if (a.gated) {
+                    if (n & 1) continue;
+                    const f4 u = acc[p0 / 16 + m][n | 1];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = w4_silu(v[k]) * u[k];
+                    col = n * 8;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) part[(m * 16 + quad * 4 + k) * 64 + ((col + c) ^ (quad * 16))] = v[k];
+            }
+        wave_lds_fence();
+        const int lanes = cols / 8, rows_at = 64 / lanes;
+        for (int r0 = 0; r0 < kRows; r0 += rows_at) {
+            const int r = r0 + lane / lanes, col = lane % lanes * 8;
+            const int in_tile = wm * 64 + p0 + r;
+            const float* from = part + r * 64 + (col ^ ((r >> 2 & 3) * 16));
+            const f4 lo = *reinterpret_cast<const f4*>(from), hi = *reinterpret_cast<const f4*>(from + 4);
+            if (tile.first + in_tile > last) continue;
+            float v[8];
+            const bool bad = s_bad[in_tile];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] = bad ? __builtin_nanf("") : lo[k];
+                v[4 + k] = bad ? __builtin_nanf("") : hi[k];
+            }
+            w4_store8(a.y, (size_t)(tile.first + in_tile) * a.N, n0 + col, a.N, v, a.y_type, A.vec_store);
+        }
+        wave_lds_fence();
+    }
+}
+
+// the instances for one type of x
+typedef void (*W4TileKernel)(W4TileArgs);
+typedef void (*W4PrepareKernel)(W4Prepare);
+template <int T>
+W4TileKernel w4_tile_pick(int WN, int S) {
+    return S == 4 ? k_w4_tile<T, 2, 4> : S == 2 ? k_w4_tile<T, 2, 2> : k_w4_tile<T, 2, 1>;
+}
+
+}  // namespace dq

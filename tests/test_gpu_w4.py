@@ -263,3 +263,25 @@ def test_weights_can_be_set_again(gpu):
         torch.cuda.synchronize()
         W.check(out, *W.want(c, 0, c["x"]), "f32", "set again")
     gpu.dq_w4_release(h)
+
+
+@pytest.mark.parametrize("type,K,rows", [("f32", 16384, 700), ("bf16", 16390, 2100)])
+def test_more_rows_than_are_prepared_at_once(gpu, type, K, rows):
+    """Long rows that are prepared for the kernel in several parts, of one
+    expert, of several, and by an index from fewer or more rows."""
+    import torch
+
+    counts = [rows // 2 - 3, 0, rows - rows // 2 - 10]
+    c = W.make(torch, 1, 3, 20, K, 128, rows, type, "f32")
+    log(f"w4 parts {type} {K} {rows}")
+    out = _grouped(gpu, torch, c, counts, tail=13)
+    _check_grouped(torch, c, counts, out)
+    r = np.random.default_rng(5)
+    for x_rows in (31, rows):
+        idx = r.integers(0, x_rows, rows).tolist()
+        d = dict(c, x=c["x"][:x_rows])
+        out = _grouped(gpu, torch, d, counts, row_index=idx, tail=13)
+        _check_grouped(torch, d, counts, out, row_index=idx)
+    one = {n: v if n in ("x", "type", "scale", "N", "K", "group", "gated") else 1 if n == "experts" else v[:1]
+           for n, v in c.items()}
+    W.check(_forward(gpu, torch, one), *W.want(one, 0, c["x"]), "f32", "one expert")
