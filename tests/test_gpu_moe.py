@@ -260,3 +260,18 @@ def test_layer_of_experts_replays(gpu):
             torch.cuda.synchronize()
             assert torch.equal(s["out"], want)
     _free_layer(gpu, s)
+
+
+def test_route_more_chunks_than_one_workgroup_sums(gpu):
+    """Over 16384 tokens, where the chunks' counts are summed by a launch of
+    their own; and fewer tokens on the same context afterwards."""
+    import torch
+
+    r = np.random.default_rng(21)
+    logits = torch.from_numpy(r.normal(0, 1, (17001, 6)).astype(np.float32))
+    logits[100:200] = -np.inf
+    h = gpu.dq_moe_init(17001, 6, 2, gpu.DQ_F32)
+    for tokens in (17001, 16385, 16384, 300):
+        got = _route(gpu, torch, logits[:tokens].cuda(), 2, h=h)
+        _check_route(got, X.route(logits[:tokens].double().numpy(), 2), f"{tokens} tokens")
+    gpu.dq_moe_release(h)
