@@ -47,6 +47,7 @@ struct W4Args {
     int gated;
     int vec;                  // rows of x can be loaded 16 bytes at a time
     int col_groups;           // workgroups along the columns
+    FastDiv per_row;          // by the pieces of 8 elements of a row, K padded to blocks
 };
 
 }  // namespace dq
@@ -71,16 +72,18 @@ struct dq_w4_ctx {
     char info[192] = "";
 };
 
-// What the files of each type of x offer: the kernel for few rows (w4_rows.h)
-// by row and column tiles of 16 a workgroup, the kernel for many (w4_tile.h) by
-// the workgroup's columns / 64, and the latter's preparation; S as above.
+// What the files of each type of x offer: the kernels for few rows (w4_rows.h,
+// and w4_any.h for rows that it cannot take) by rows and column tiles of 16 a
+// workgroup, the kernel for many (w4_tile.h) by the workgroup's columns / 64,
+// and the latter's preparation; S as above.
 namespace dq {
 
 struct W4TileArgs;
 struct W4Prepare;
 struct W4Kernels {
-    void (*(*rows)(int row_tiles, int col_tiles, int S))(W4Args);
-    void (*(*tile)(int wide, int S))(W4TileArgs);
+    void (*(*rows)(int rows, int col_tiles, int S, int scales))(W4Args);
+    void (*(*any)(int rows, int col_tiles, int S))(W4Args);
+    void (*(*tile)(int S, int scales, bool gather))(W4TileArgs);
     void (*prepare)(W4Prepare);
 };
 W4Kernels w4_kernels_bf16();

@@ -1,5 +1,6 @@
 // w4.hip -- products with 4-bit weights and group scales: contexts, packing
 // and the entry points. The formula and the layout are in w4.h.
+#include "w4_rows.h"
 #include "w4_tile.h"
 
 #include <algorithm>
@@ -10,6 +11,8 @@ namespace {
 
 using namespace dq;
 
+// bytes of x that the kernel for few rows takes to LDS
+constexpr int64_t kXLds = 64 << 10;
 // rows an expert from which the kernel for many rows is taken
 constexpr int kTileMean = 64;
 // bytes that a context keeps for prepared rows; more rows go in several launches
@@ -116,9 +119,9 @@ W4Args forward_args(const dq_w4_ctx* c, const void* x, int64_t x_row_stride, voi
     A.scale_type = c->scale_type;
     A.y_type = c->y_type;
     A.gated = c->gated;
-    // 16 bytes at a time: every row starts at one, and K ends at one
+    // 8 elements at a time, 16 bytes each load: rows start at a multiple of those, and K ends at one
     const int per16 = 16 / elem_bytes(c->x_type);
-    A.vec = (uintptr_t)x % 16 == 0 && x_row_stride % per16 == 0 && c->K % per16 == 0;
+    A.vec = (uintptr_t)x % 16 == 0 && x_row_stride % per16 == 0 && c->K % 8 == 0;
     return A;
 }
 
@@ -127,19 +130,53 @@ W4Kernels kernels_of(const dq_w4_ctx* c) {
 }
 
 int launch_rows(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
-    // row tiles by the mean rows of an expert: more tiles read the weights once for more rows
+    const bool gated = c->gated;
+    const int used = (c->N + 15) / 16 * (gated ? 2 : 1), least = gated ? 2 : 1;
     const int mean = A.offsets ? (A.rows + c->experts - 1) / c->experts : A.rows;
-    const int row_tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4, TM = row_tiles * 16;
-    const int col_tiles = c->gated ? 2 : 1;
-    const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
-    A.col_groups = used / col_tiles;
+    // rows that start 16 bytes apart, in reach of 31 bits
+    const __int128 reach = (__int128)(A.row_index ? A.x_rows : 64) * A.x_stride + A.K;
+    const bool fast = A.vec && reach * elem_bytes(c->x_type) < (__int128)kW4Far;
+    int TM, col_tiles, waves;
+    bool in_lds = false;
+    const int64_t x_row = ((int64_t)c->blocks * kW4Block * 2 + 64) * (c->x_type == DQ_F32 ? 3 : 1);
+    if (fast) {
+        // experts' rows differ: twice the mean in one tile of rows
+        const int rows = A.offsets ? 2 * mean : mean;
+        auto fits = [&](int tm) { return (A.offsets ? tm : std::min(tm, A.rows)) * x_row <= kXLds; };
+        TM = rows <= 4 && fits(4) ? 4 : rows >= 64 ? 64 : (rows + 15) / 16 * 16;
+        in_lds = TM == 4;
+    } else {
+        TM = mean <= 16 ? 16 : 64;
+    }
+    const int row_tiles = (TM + 15) / 16;
     const int64_t tiles_m = A.offsets ? (int64_t)A.rows / TM + std::min(A.rows, c->experts) : (A.rows + TM - 1) / TM;
+    if (fast) {
+        // Wide workgroups read x less often (rows of 48: 4 column tiles take half
+        // the time of 1), as long as there are waves for the whole chip: 16 a
+        // compute unit, 8 of those that hold many sums
+        const int narrow = in_lds ? least : 2;
+        col_tiles = 4;
+        auto most = [&](int ct) { return std::min(row_tiles * ct >= 3 ? 8 : 16, c->blocks); };
+        auto want = [&](int ct) { return (int64_t)c->cus * (row_tiles * ct >= 3 ? 8 : 16); };
+        while (col_tiles > narrow && tiles_m * (used / col_tiles) * most(col_tiles) < want(col_tiles)) col_tiles /= 2;
+        waves = 1;
+        while (waves * 2 <= most(col_tiles) && tiles_m * (used / col_tiles) * waves < want(col_tiles)) waves *= 2;
+    } else {
+        col_tiles = least;
+        waves = 8;
+        while (waves > 1 && waves / 2 >= c->blocks) waves /= 2;
+    }
+    A.col_groups = (used + col_tiles - 1) / col_tiles;
     const int64_t grid = tiles_m * A.col_groups;
     if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
-    int waves = 8;
-    while (waves > 1 && waves / 2 >= c->blocks) waves /= 2;
-    const size_t lds = (size_t)waves * col_tiles * row_tiles * 1024;
-    hipLaunchKernelGGL(kernels_of(c).rows(row_tiles, col_tiles, c->S), dim3((unsigned)grid), dim3(waves * 64), lds, s, A);
+    const W4Kernels k = kernels_of(c);
+    const int parts = waves * col_tiles * row_tiles;
+    size_t lds = (size_t)(parts > 64 && fast ? parts / 2 : parts) * (TM == 4 ? 256 : 1024);
+    if (in_lds) lds = std::max(lds, (size_t)((A.offsets ? TM : std::min(TM, A.rows)) * x_row));
+    A.per_row = make_fastdiv((uint32_t)c->blocks * (kW4Block / 8));
+    const W4RowsKernel f = fast ? k.rows(TM, col_tiles, c->S, c->scale_type) : k.any(TM, col_tiles, c->S);
+    if (!f) DQ_FAIL(DQ_ERR_RANGE, "no kernel of %d rows by %d column tiles", TM, col_tiles);
+    hipLaunchKernelGGL(f, dim3((unsigned)grid), dim3(waves * 64), lds, s, A);
     DQ_LAUNCH_CHECK("product with 4-bit weights");
     return DQ_OK;
 }
@@ -207,7 +244,7 @@ int launch_tile(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
         const int64_t grid = (units() + 7) / 8 * 8 * T.gm * T.gn;
         if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
         T.vec_store = (uintptr_t)A.y % 16 == 0 && c->N % 8 == 0;
-        hipLaunchKernelGGL(k.tile(wide, c->S), dim3((unsigned)grid), dim3(128 * wide), 0, s, T);
+        hipLaunchKernelGGL(k.tile(c->S, c->scale_type, A.row_index && !T.x_by_row), dim3((unsigned)grid), dim3(128 * wide), 0, s, T);
         DQ_LAUNCH_CHECK("product with 4-bit weights");
     }
     return DQ_OK;

@@ -6,6 +6,7 @@
 
 namespace dq {
 
+typedef void (*W4RowsKernel)(W4Args);
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
@@ -84,11 +85,11 @@ __device__ __forceinline__ void w4_load8(const char* row, int k, int K, bool vec
     if constexpr (T == DQ_F32) {
         float v[8];
         if (vec) {
-            // K is a multiple of 4 here: each half lies inside or outside the row
+            // K is a multiple of 8 here
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 f4 t = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (k + 4 * h < K) t = *reinterpret_cast<const f4*>(p + 16 * h);
+                if (k < K) t = *reinterpret_cast<const f4*>(p + 16 * h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[4 * h + i] = t[i];
             }
@@ -115,6 +116,30 @@ __device__ __forceinline__ float w4_scale(const void* scales, size_t i, int type
     if (type == DQ_F32) return static_cast<const float*>(scales)[i];
     const uint16_t b = static_cast<const uint16_t*>(scales)[i];
     return type == DQ_BF16 ? bf16_bits_to_f32(b) : (float)__builtin_bit_cast(_Float16, b);
+}
+
+// A column's scales of a block: N bytes as words, and the g-th of them.
+template <int N>
+__device__ __forceinline__ void w4_words(const char* p, uint32_t* w) {
+    if constexpr (N == 2) {
+        w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (N == 4) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 8) {
+        const u2 t = *reinterpret_cast<const u2*>(p);
+        w[0] = t[0];
+        w[1] = t[1];
+    } else {
+        const u4 t = *reinterpret_cast<const u4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = t[i];
+    }
+}
+template <int ST>
+__device__ __forceinline__ float w4_scale_word(const uint32_t* w, int g) {
+    if constexpr (ST == DQ_F32) return __uint_as_float(w[g]);
+    const uint32_t h = w[g / 2] >> (16 * (g & 1)) & 0xffffu;
+    return ST == DQ_BF16 ? bf16_bits_to_f32(h) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
 }
 
 __device__ __forceinline__ void w4_store(void* y, size_t i, float v, int type) {
@@ -178,12 +203,11 @@ __device__ __forceinline__ W4Tile w4_tile(const W4Args& A, int t, int TM, int lo
             const int v = __shfl_up(upto, o);
             if (lane >= o) upto += v;
         }
-        const int total = __shfl(upto, 63);
+        const int total = __builtin_amdgcn_readlane(upto, 63);  // uniform, and seen as such
         if (t < before + total) {
             const int l = __ffsll((unsigned long long)__ballot(before + upto > t)) - 1;
-            const int first = __shfl(a, l) + (t - before - __shfl(upto - n, l)) * TM;
-            return {__builtin_amdgcn_readfirstlane(e0 + l), __builtin_amdgcn_readfirstlane(first),
-                    __builtin_amdgcn_readfirstlane(min(first + TM, __shfl(b, l)))};
+            const int first = __builtin_amdgcn_readlane(a, l) + (t - before - __builtin_amdgcn_readlane(upto - n, l)) * TM;
+            return {e0 + l, first, min(first + TM, __builtin_amdgcn_readlane(b, l))};
         }
         before += total;
     }

@@ -1,9 +1,12 @@
 // w4_f16.hip -- the 4-bit weights' kernels for fp16 rows of x.
+#include "w4_any.h"
 #include "w4_rows.h"
 #include "w4_tile.h"
 
 namespace dq {
 
-W4Kernels w4_kernels_f16() { return {w4_rows_pick<DQ_F16>, w4_tile_pick<DQ_F16>, k_w4_prepare<DQ_F16>}; }
+W4Kernels w4_kernels_f16() {
+    return {w4_rows_pick<DQ_F16>, w4_any_pick<DQ_F16>, w4_tile_pick<DQ_F16>, k_w4_prepare<DQ_F16>};
+}
 
 }  // namespace dq

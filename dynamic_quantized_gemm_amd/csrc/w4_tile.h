@@ -25,7 +25,8 @@
 
 namespace dq {
 
-constexpr int kW4TileRows = 128;
+constexpr int kW4TileM = 4;  // row tiles of 16 of a wave
+constexpr int kW4TileRows = 2 * 16 * kW4TileM;
 
 // Rows of x as the tile kernel takes them, and the sums of their groups.
 struct W4Prepare {
@@ -87,10 +88,12 @@ struct W4TileArgs {
     int vec_store;
 };
 
-template <int T, int WN, int S>
+// G: the rows of x are looked up in row_index. ST: the scales' type.
+template <int T, int WN, int S, int ST, bool G>
 __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
     using O = W4Op<T>;
-    constexpr int P = O::P, NW = 2 * WN, CPW = 32 / NW;  // waves, copies a wave and stage
+    constexpr int P = O::P, NW = 2 * WN, CPW = kW4TileRows / 4 / NW;  // waves, copies a wave and stage
+    constexpr int SB = ST == DQ_F32 ? 4 : 2, SW = (S * SB + 3) / 4;  // words of a column's scales
     __shared__ __attribute__((aligned(16))) char st0[kW4TileRows * 256];
     __shared__ __attribute__((aligned(16))) char st1[kW4TileRows * 256];
     __shared__ __attribute__((aligned(16))) float s_sum[2][S][kW4TileRows];
@@ -111,75 +114,98 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
     if (tile.first >= tile.end) return;
 
     // Copies of x: each takes 4 rows of 256 bytes, lane l the 16-byte piece (l %
-    // 16) ^ (row % 16) of row l / 16, to LDS in the order of the lanes.
+    // 16) ^ (row % 16) of row l / 16, to LDS in the order of the lanes. Without an
+    // index the rows of copies i and i + 4 differ by a distance alone.
     const int last = tile.end - 1;
-    uint32_t voff[CPW];
-    const bool gather = a.row_index && !A.x_by_row;
-    const long long row0 = gather ? 0 : tile.first - (A.x_by_row ? A.row_lo : 0);
-    const char* xbase = static_cast<const char*>(a.x) + row0 * a.x_stride * 2;
+    constexpr int NV = G ? CPW : 4;
+    static_assert(CPW * NW * 4 == kW4TileRows, "every wave copies the same rows");
+    uint32_t voff[NV];
+    const int row0 = G ? 0 : tile.first - (A.x_by_row ? A.row_lo : 0);
+    const uint32_t x_bytes = (uint32_t)(a.x_stride * 2);
+    const int rows_here = tile.end - tile.first;
+    // ends with the last row: one past the tile's end reads as zeros, or as a row that is there
+    const uint32_t x_end = (uint32_t)((G ? a.x_rows : rows_here) - 1) * x_bytes + (uint32_t)(P * a.blocks) * (kW4Block * 2);
+    __amdgpu_buffer_rsrc_t xbuf = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(a.x) + (long long)row0 * a.x_stride * 2), 0, (int)x_end, 0x00027000);
 #pragma unroll
     for (int i = 0; i < CPW; ++i) {
-        const int r = (wave * CPW + i) * 4 + quad, at = min(tile.first + r, last);
-        int src = a.row_index ? a.row_index[at] : 0;
-        const bool bad = a.row_index && (src < 0 || src >= a.x_rows);
-        if (c == 0) s_bad[r] = bad;
-        if (!gather) src = at - tile.first;
-        else if (bad) src = 0;
-        voff[i] = (uint32_t)((long long)src * a.x_stride * 2) + (uint32_t)((c ^ (r & 15)) * 16);
+        const int r = (wave * CPW + i) * 4 + quad;
+        int src = min(r, rows_here - 1);
+        if (a.row_index) {
+            const int at = a.row_index[tile.first + src];
+            const bool bad = at < 0 || at >= a.x_rows;
+            if (G) src = bad ? 0 : at;
+            if (c == 0) s_bad[r] = bad;
+        } else if (c == 0) {
+            s_bad[r] = false;
+        }
+        if (i < NV) voff[i] = (uint32_t)(G ? src : r) * x_bytes + (uint32_t)((c ^ (r & 15)) * 16);
     }
     auto copy = [&](int stage_k, char* dst) {
         // stage_k: the element of a row at which the stage's 128 begin
 #pragma unroll
-        for (int i = 0; i < CPW; ++i) copy16_to_lds(xbase + (size_t)stage_k * 2 + voff[i], dst + (wave * CPW + i) * 1024);
+        for (int i = 0; i < CPW; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                xbuf, (__attribute__((address_space(3))) void*)(dst + (wave * CPW + i) * 1024), 16,
+                (int)voff[i % NV], (int)((uint32_t)stage_k * 2 + (uint32_t)(i / NV * 16) * x_bytes), 0, 0);
     };
-    // the sums of x of thread t's row (t < 128)
-    const float* sum_row;
+    // the sums of x of thread t's row, as an offset (they take less than 2^32 bytes)
+    uint32_t sum_at;
     {
-        const int r = min(tile.first + (int)(threadIdx.x & (kW4TileRows - 1)), last);
+        const int r = min(tile.first + (int)threadIdx.x, last);
         int src = r;
         if (A.by_row) src = r - A.row_lo;
         else if (a.row_index) {
             src = a.row_index[r];
             if (src < 0 || src >= a.x_rows) src = 0;
         }
-        sum_row = A.sums + (size_t)src * a.blocks * S;
+        sum_at = (uint32_t)src * (uint32_t)(a.blocks * S) * 4u;
     }
     const int nt0 = tn * (WN * 4) + wn * 4;  // this wave's column tiles
     const size_t base = (size_t)tile.expert * a.tiles + nt0;
-    const u4* codes = reinterpret_cast<const u4*>(a.codes) + base * a.blocks * 64 + lane;
-    const size_t code_step = (size_t)a.blocks * 64;
+    // uniform addresses, and each lane's part of them
+    const char* codes = reinterpret_cast<const char*>(a.codes) + base * a.blocks * 1024;
+    const char* scales = static_cast<const char*>(a.scales) + base * a.blocks * (16 * S * SB);
+    const uint32_t code_at = lane * 16, scale_at = c * (S * SB);
 
-    f4 acc[4][4];
+    f4 acc[kW4TileM][4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < kW4TileM; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n) acc[m][n] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     u4 code[2][4];
-    float sc[2][4][S], sum[S];
+    uint32_t sc[2][4][SW];  // a column's scales as they lie in memory
+    float sum[S];
     const int nstages = a.blocks * P, Kp = a.blocks * kW4Block;
 
-    auto fetch = [&](int b, u4* w, float (*s)[S]) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n) w[n] = codes[n * code_step + (size_t)b * 64];
+    auto fetch = [&](int b, u4* w, uint32_t (*s)[SW]) {
 #pragma unroll
         for (int n = 0; n < 4; ++n)
+            w[n] = *reinterpret_cast<const u4*>(codes + ((size_t)n * a.blocks + b) * 1024 + code_at);
 #pragma unroll
-            for (int g = 0; g < S; ++g)
-                s[n][g] = w4_scale(a.scales, (((base + n) * a.blocks + b) * 16 + c) * S + g, a.scale_type);
+        for (int n = 0; n < 4; ++n) w4_words<S * SB>(scales + ((size_t)n * a.blocks + b) * (16 * S * SB) + scale_at, s[n]);
     };
     auto fetch_sums = [&](int b) {
+        const char* p = reinterpret_cast<const char*>(A.sums) + b * (S * 4) + sum_at;
 #pragma unroll
-        for (int g = 0; g < S; ++g) sum[g] = sum_row[b * S + g];
+        for (int g = 0; g < S; ++g) sum[g] = reinterpret_cast<const float*>(p)[g];
     };
 
     copy(0, st0);
     fetch(0, code[0], sc[0]);
-    if (threadIdx.x < kW4TileRows) fetch_sums(0);
+    fetch_sums(0);
 
+    // One stage: 4 steps of 32 k, each 16 products of a wave, column by column: a
+    // column's operand is free after its 4, and the next step's is unpacked into it
+    // while the next column's run; behind a group's last step its sums are scaled and
+    // added likewise. The scheduling groups put these between the products.
+    u4 w[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) w[n] = O::codes(code[0][n][0]);
     auto stage = [&](auto CUR, int i) {
         constexpr int cur = decltype(CUR)::value;
         const char* L = cur ? st1 : st0;
-        if (threadIdx.x < kW4TileRows)
+        if ((int)threadIdx.x < kW4TileRows)
 #pragma unroll
             for (int g = 0; g < S; ++g) s_sum[cur][g][threadIdx.x] = sum[g];
         wait_vmcnt_lgkm0<0>();
@@ -187,41 +213,68 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
         // past the end the last stage again: in bounds, not used
         const int nx = min(i + 1, nstages - 1), nb = P == 1 ? nx : nx / P;
         copy(nb * kW4Block + (nx - nb * P) * Kp, cur ? st0 : st1);
-        fetch(nb, code[cur ^ 1], sc[cur ^ 1]);
-        if (threadIdx.x < kW4TileRows) fetch_sums(nb);
         const bool first = P == 1 || i % P == 0;
+        u4 x[2][kW4TileM];
+        auto read_x = [&](u4* to, int q) {
 #pragma unroll
-        for (int g = 0; g < S; ++g) {
-            f4 t[4][4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f4 t0 = *reinterpret_cast<const f4*>(&s_sum[cur][g][wm * 64 + m * 16 + quad * 4]);
-                if (!first) t0 = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int n = 0; n < 4; ++n) t[m][n] = t0;
+            for (int m = 0; m < kW4TileM; ++m) {
+                const int r = wm * (16 * kW4TileM) + m * 16 + c;
+                to[m] = *reinterpret_cast<const u4*>(L + r * 256 + (((q * 4 + quad) ^ c) * 16));
             }
+        };
+        read_x(x[0], 0);
+        f4 t[kW4TileM][4];
 #pragma unroll
-            for (int q = g * (4 / S); q < (g + 1) * (4 / S); ++q) {
-                u4 x[4], w[4];
+        for (int q = 0; q < 4; ++q) {
+            constexpr int per = 4 / S;
+            const int g = q / per;
+            const bool begins = q % per == 0, ends = (q + 1) % per == 0;
+            __builtin_amdgcn_sched_barrier(0);
+            if (begins)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int r = wm * 64 + m * 16 + c;
-                    x[m] = *reinterpret_cast<const u4*>(L + r * 256 + (((q * 4 + quad) ^ c) * 16));
+                for (int m = 0; m < kW4TileM; ++m) {
+                    f4 t0 = *reinterpret_cast<const f4*>(&s_sum[cur][g][wm * (16 * kW4TileM) + m * 16 + quad * 4]);
+                    if (!first) t0 = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) t[m][n] = t0;
                 }
-#pragma unroll
-                for (int n = 0; n < 4; ++n) w[n] = O::codes(code[cur][n][q]);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) t[m][n] = O::mfma(x[m], w[n], t[m][n]);
+            if (q < 3) read_x(x[(q + 1) & 1], q + 1);
+            if (q == 1) {  // half a stage ahead: registers are scarce before
+                fetch(nb, code[cur ^ 1], sc[cur ^ 1]);
+                fetch_sums(nb);
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int n = 0; n < 4; ++n) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int m = 0; m < kW4TileM; ++m) t[m][n] = O::mfma(x[q & 1][m], w[n], t[m][n]);
+                // behind the last step the next stage's first
+                w[n] = O::codes(q < 3 ? code[cur][n][q + 1] : code[cur ^ 1][n][0]);
+                if (ends) {
+                    const float s = w4_scale_word<ST>(sc[cur][n], g);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(sc[cur][n][g], t[m][n][v], acc[m][n][v]);
-            if (g + 1 < S) __builtin_amdgcn_sched_barrier(0);  // one group's sums in registers at a time
+                    for (int m = 0; m < kW4TileM; ++m)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(s, t[m][n][v], acc[m][n][v]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4 * kW4TileM; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);                 // a product
+                if (k < 2 * kW4TileM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // an LDS read
+                if (k >= kW4TileM) {                                                    // vector operations
+                    if (ends) __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+                    else __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
+                }
+            }
+            // results are due here: left to itself the compiler moves the additions into the
+            // next stage, and keeps every group's sums until then
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                asm volatile("" : "+v"(w[n]));
+                if (ends)
+#pragma unroll
+                    for (int m = 0; m < kW4TileM; ++m) asm volatile("" : "+v"(acc[m][n]));
+            }
         }
     };
     int i = 0;
@@ -253,8 +306,8 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
                 split3(v, &zs[n][0], &zs[n][1], &zs[n][2]);
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int r = min(tile.first + wm * 64 + m * 16 + c, last);
+            for (int m = 0; m < kW4TileM; ++m) {
+                const int r = min(tile.first + wm * (16 * kW4TileM) + m * 16 + c, last);
                 int src = A.by_row ? r - A.row_lo : r;
                 if (!A.by_row && a.row_index) {
                     src = a.row_index[r];
@@ -280,10 +333,10 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
         }
     }
 
-    // bias and gate, through this wave's part of the stages (32 rows at a time)
+    // bias and gate, through this wave's part of the stages 
     // so that whole rows go out, 16 bytes a lane
-    constexpr int kPart = 2 * kW4TileRows * 256 / NW;  // 16 KiB or 8
-    constexpr int kRows = kPart / 256 < 64 ? kPart / 256 : 64;
+    constexpr int kPart = 2 * kW4TileRows * 256 / NW, kRows = 16 * kW4TileM;
+    static_assert(kPart >= kRows * 256, "a wave's rows of 64 in fp32");
     char* part_base = wave < NW / 2 ? st0 + wave * kPart : st1 + (wave - NW / 2) * kPart;
     float* part = reinterpret_cast<float*>(part_base);
     const int cols = a.gated ? 32 : 64;
@@ -293,21 +346,20 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
         for (int n = 0; n < 4; ++n) {
             const float bias = a.bias[(base + n) * 16 + c];
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < kW4TileM; ++m)
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[m][n][v] += bias;
         }
+    {
 #pragma unroll
-    for (int p0 = 0; p0 < 64; p0 += kRows) {
-#pragma unroll
-        for (int m = 0; m < kRows / 16; ++m)
+        for (int m = 0; m < kW4TileM; ++m)
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                f4 v = acc[p0 / 16 + m][n];
+                f4 v = acc[m][n];
                 int col = n * 16;
                 if (a.gated) {
                     if (n & 1) continue;
-                    const f4 u = acc[p0 / 16 + m][n | 1];
+                    const f4 u = acc[m][n | 1];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = w4_silu(v[k]) * u[k];
                     col = n * 8;
@@ -319,7 +371,7 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
         const int lanes = cols / 8, rows_at = 64 / lanes;
         for (int r0 = 0; r0 < kRows; r0 += rows_at) {
             const int r = r0 + lane / lanes, col = lane % lanes * 8;
-            const int in_tile = wm * 64 + p0 + r;
+            const int in_tile = wm * kRows + r;
             const float* from = part + r * 64 + (col ^ ((r >> 2 & 3) * 16));
             const f4 lo = *reinterpret_cast<const f4*>(from), hi = *reinterpret_cast<const f4*>(from + 4);
             if (tile.first + in_tile > last) continue;
@@ -339,9 +391,21 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
 // the instances for one type of x
 typedef void (*W4TileKernel)(W4TileArgs);
 typedef void (*W4PrepareKernel)(W4Prepare);
+template <int T, int WN, int S, int ST>
+W4TileKernel w4_tile_pick(bool gather) {
+    return gather ? k_w4_tile<T, WN, S, ST, true> : k_w4_tile<T, WN, S, ST, false>;
+}
+template <int T, int WN, int S>
+W4TileKernel w4_tile_pick(int scales, bool g) {
+    return scales == DQ_F32    ? w4_tile_pick<T, WN, S, DQ_F32>(g)
+           : scales == DQ_BF16 ? w4_tile_pick<T, WN, S, DQ_BF16>(g)
+                               : w4_tile_pick<T, WN, S, DQ_F16>(g);
+}
 template <int T>
-W4TileKernel w4_tile_pick(int WN, int S) {
-    return S == 4 ? k_w4_tile<T, 2, 4> : S == 2 ? k_w4_tile<T, 2, 2> : k_w4_tile<T, 2, 1>;
+W4TileKernel w4_tile_pick(int S, int scales, bool gather) {
+    return S == 4   ? w4_tile_pick<T, 2, 4>(scales, gather)
+           : S == 2 ? w4_tile_pick<T, 2, 2>(scales, gather)
+                    : w4_tile_pick<T, 2, 1>(scales, gather);
 }
 
 }  // namespace dq
