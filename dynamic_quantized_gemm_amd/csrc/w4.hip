@@ -156,10 +156,12 @@ int launch_rows(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
         // compute unit, 8 of those that hold many sums
         const int narrow = in_lds ? least : 2;
         col_tiles = 4;
-        auto most = [&](int ct) { return std::min(row_tiles * ct >= 3 ? 8 : 16, c->blocks); };
-        auto want = [&](int ct) { return (int64_t)c->cus * (row_tiles * ct >= 3 ? 8 : 16); };
+        auto most = [&](int ct) {
+            return std::min(in_lds && ct <= 2 ? 16 : !in_lds && c->x_type == DQ_F32 && row_tiles >= 3 ? 4 : 8, c->blocks);
+        };
+        auto want = [&](int ct) { return (int64_t)c->cus * (in_lds && ct <= 2 ? 16 : 8); };
         while (col_tiles > narrow && tiles_m * (used / col_tiles) * most(col_tiles) < want(col_tiles)) col_tiles /= 2;
-        waves = 1;
+        waves = std::min(in_lds ? 1 : 4, most(col_tiles));
         while (waves * 2 <= most(col_tiles) && tiles_m * (used / col_tiles) * waves < want(col_tiles)) waves *= 2;
     } else {
         col_tiles = least;
@@ -170,9 +172,11 @@ int launch_rows(const dq_w4_ctx* c, W4Args A, hipStream_t s) {
     const int64_t grid = tiles_m * A.col_groups;
     if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
     const W4Kernels k = kernels_of(c);
-    const int parts = waves * col_tiles * row_tiles;
-    size_t lds = (size_t)(parts > 64 && fast ? parts / 2 : parts) * (TM == 4 ? 256 : 1024);
-    if (in_lds) lds = std::max(lds, (size_t)((A.offsets ? TM : std::min(TM, A.rows)) * x_row));
+    // LDS that the launch brings: rows of x or the waves' parts, 64 KiB at most; the
+    // rings are the kernel's own
+    size_t lds = 0;
+    if (!fast) lds = (size_t)waves * col_tiles * row_tiles * 1024;
+    else if (in_lds) lds = std::max((size_t)waves * col_tiles * 256, (size_t)((A.offsets ? TM : std::min(TM, A.rows)) * x_row));
     A.per_row = make_fastdiv((uint32_t)c->blocks * (kW4Block / 8));
     const W4RowsKernel f = fast ? k.rows(TM, col_tiles, c->S, c->scale_type) : k.any(TM, col_tiles, c->S);
     if (!f) DQ_FAIL(DQ_ERR_RANGE, "no kernel of %d rows by %d column tiles", TM, col_tiles);

@@ -27,6 +27,13 @@ __device__ __forceinline__ void split3(const float* v, u4* hi, u4* mid, u4* lo) 
     }
 }
 
+// 16 bytes a lane from a bounded buffer straight into LDS, the wave's lanes one behind
+// the other from `block` (uniform) on; zeros for an offset beyond the buffer. A plain
+// device function: in a lambda it would be compiled for the host too.
+__device__ __forceinline__ void buffer16_to_lds(__amdgpu_buffer_rsrc_t buf, char* block, uint32_t lane_at, uint32_t at) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (__attribute__((address_space(3))) void*)block, 16, (int)lane_at, (int)at, 0, 0);
+}
+
 // The matrix operands that a type of x is multiplied in, P pieces of it.
 template <int T>
 struct W4Op;

@@ -5,17 +5,19 @@
 // W-th block of 128 of K, so together they read one stream, and their partial
 // sums meet in LDS in a fixed order.
 //
-// The operands: A = 16 rows of x, B = 16 columns' codes. A row past the tile's
-// end and a k past K are offsets out of the buffer's range: such a load returns
-// zeros and moves nothing, without a branch, so the waits are exact. Loads
-// return in the order of their issue, codes from the memory, x from the caches:
-// a wait for x is one for every code that was asked for before it. So up to 4
-// rows of x go to LDS first, and codes are on their way two or three blocks
-// ahead (16 rows of 1400 in LDS: no faster, they fill it); of more rows, x comes from the caches a block ahead, a
-// pair of steps of 32 at a time (the two halves of a cache line), and codes
-// with it. The sum of a group's x, which its zero point multiplies, is one
-// more product, with ones: in the accumulators' layout without any exchange,
-// on matrix cores that are idle most of the time here.
+// The operands: A = 16 rows of x, B = 16 columns' codes. x comes through LDS:
+// straight from the caches the operand takes 16 bytes of 16 rows from
+// neighbouring lanes, and each is an access of its own (64 cycles a load, 48
+// rows of 16384 x 4096: 13.5 us per 4096 of K, 5.6 of them the codes'). Up to 4
+// rows are put there whole before the loop. Of more, each wave keeps a ring of
+// two half blocks of 64 k for itself, filled by loads of whole lines straight to
+// LDS. A row past the tile's end and a k past K are offsets out of the buffer's
+// range: such a load gives zeros and moves nothing, without a branch, so the
+// waits are exact. Loads return in the order of their issue: codes are asked
+// for a block (or more) ahead, behind the x that is needed before them.
+// The sum of a group's x, which its zero point multiplies, is one more
+// product, with ones: in the accumulators' layout without any exchange, on
+// matrix cores that are idle most of the time here.
 #pragma once
 
 #include "w4_device.h"
@@ -24,24 +26,30 @@ namespace dq {
 
 constexpr uint32_t kW4Far = 0x80000000u;  // the buffer's size: an offset from here on reads as zeros
 
-// Eight elements of x for one lane, as they lie in memory.
-template <int T>
-struct W4X {
-    u4 v[W4Op<T>::elem / 2];
-};
+// The most waves of a workgroup: by their registers, and by their rings.
+template <int T, int RT, int CT, int V>
+constexpr int w4_rows_waves() {
+    return V == 1 && CT <= 2 ? 16 : V == 4 && T == DQ_F32 && RT >= 3 ? 4 : 8;
+}
 
 // V: rows of y that a lane holds of a tile. The four lanes with the same column hold
 // 4 V rows: 16, or 4 where there are no more (row m of x then lies in the operand's
 // row 4 m, so that a lane's first value is all that it scales and adds).
 // ST: the scales' type.
 template <int T, int RT, int CT, int S, int ST, int V>
-__global__ void __launch_bounds__(RT * CT >= 3 ? 512 : 1024) k_w4_rows(W4Args A) {
+__global__ void __launch_bounds__((w4_rows_waves<T, RT, CT, V>() * 64)) k_w4_rows(W4Args A) {
     using O = W4Op<T>;
     constexpr int P = O::P, TM = RT * 4 * V, SB = ST == DQ_F32 ? 4 : 2;
-    constexpr bool XL = V == 1;  // x through LDS
-    static_assert(!XL || RT == 1, "one tile of rows in LDS");
+    constexpr bool WHOLE = V == 1;  // the rows of x lie in LDS whole
+    static_assert(!WHOLE || RT == 1, "one tile of rows");
     typedef float fv __attribute__((ext_vector_type(V)));
+    // a ring's half blocks in arrays of their own: a read of one is then known not to
+    // depend on a load to the other
+    constexpr int kHalfRow = 64 * O::elem, kHalf = TM * kHalfRow;
+    constexpr int kRing = WHOLE ? 16 : w4_rows_waves<T, RT, CT, V>() * kHalf;
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    __shared__ __attribute__((aligned(16))) char ring0[kRing];
+    __shared__ __attribute__((aligned(16))) char ring1[kRing];
     __shared__ int s_bad[TM];
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -51,145 +59,153 @@ __global__ void __launch_bounds__(RT * CT >= 3 ? 512 : 1024) k_w4_rows(W4Args A)
     if (tile.first >= tile.end) return;
     const int t0 = group * CT;
 
-    // this lane's rows of x, as offsets in bytes from the first one's (with an index
-    // from x's)
-    const long long row0 = A.row_index ? 0 : tile.first;
-    __amdgpu_buffer_rsrc_t xbuf = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(static_cast<const char*>(A.x) + row0 * A.x_stride * O::elem), 0, (int)kW4Far, 0x00027000);
-    uint32_t row[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int m = V == 4 ? r * 16 + c : c >> 2, i = tile.first + m;
-        const bool one = V == 4 || (c & 3) == 0;  // a lane that holds a row
-        int src = min(i, tile.end - 1);
-        if (A.row_index) src = A.row_index[src];
-        const bool bad = A.row_index && (src < 0 || src >= A.x_rows);
-        row[r] = i >= tile.end || bad || !one ? kW4Far : (uint32_t)((src - (int)row0) * A.x_stride * O::elem);
-        if (wave == 0 && quad == 0 && one) s_bad[m] = bad;
-    }
-
     const size_t base = (size_t)tile.expert * A.tiles + t0;
-    const u4* codes = reinterpret_cast<const u4*>(A.codes) + base * A.blocks * 64 + lane;
-    const char* scales = static_cast<const char*>(A.scales) + (base * A.blocks * 16 + c) * (S * SB);
-    const uint8_t* zeros = A.zeros + (base * A.blocks * 16 + c) * S;
+    const char* codes = reinterpret_cast<const char*>(A.codes) + base * A.blocks * 1024;
+    const char* scales = static_cast<const char*>(A.scales) + base * A.blocks * (16 * S * SB);
+    // without zero points a buffer of no size, whose zeros become 8
+    __amdgpu_buffer_rsrc_t zbuf = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(A.zeros) + (A.zeros ? base * A.blocks * (16 * S) : 0), 0, A.zeros ? (int)kW4Far : 0, 0x00027000);
+    const uint32_t z_default = A.zeros ? 0u : 0x08080808u;
+    const uint32_t code_at = lane * 16, scale_at = c * (S * SB);
 
     struct Block {
         u4 code[CT];
         uint32_t scale[CT][(S * SB + 3) / 4];
         uint32_t zero[CT];
     };
-    auto fetch = [&](Block& k, int b) {
+    const int last = A.blocks - 1;
+    // past the end the last block again: in bounds, not used
+    auto fetch = [&](Block& k, int at) {
+        const int b = min(at, last);
 #pragma unroll
-        for (int j = 0; j < CT; ++j) k.code[j] = codes[((size_t)j * A.blocks + b) * 64];
+        for (int j = 0; j < CT; ++j)
+            k.code[j] = *reinterpret_cast<const u4*>(codes + ((size_t)j * A.blocks + b) * 1024 + code_at);
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            const size_t at = ((size_t)j * A.blocks + b) * 16;
-            w4_words<S * SB>(scales + at * (S * SB), k.scale[j]);
-            if (A.zeros) {
-                const uint8_t* z = zeros + at * S;
-                if constexpr (S == 4) k.zero[j] = *reinterpret_cast<const uint32_t*>(z);
-                else if constexpr (S == 2) k.zero[j] = *reinterpret_cast<const uint16_t*>(z);
-                else k.zero[j] = *z;
-            } else {
-                k.zero[j] = 0x08080808u;
-            }
+            w4_words<S * SB>(scales + ((size_t)j * A.blocks + b) * (16 * S * SB) + scale_at, k.scale[j]);
+            const int z = (j * A.blocks + b) * (16 * S);
+            if constexpr (S == 4) k.zero[j] = __builtin_amdgcn_raw_buffer_load_b32(zbuf, c * S, z, 0);
+            else if constexpr (S == 2) k.zero[j] = __builtin_amdgcn_raw_buffer_load_b16(zbuf, c * S, z, 0);
+            else k.zero[j] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, c * S, z, 0);
         }
     };
-    // x in LDS: [P][rows][K padded, and 64 bytes], so that the rows of an operand begin in
-    // different banks; a lane without a row reads another's (not stored)
-    const int x_stride = A.blocks * (kW4Block * 2) + 64, x_rows = min(tile.end - tile.first, TM);
-    const int x_at = min(V == 4 ? c : c >> 2, x_rows - 1) * x_stride + quad * 16;
-    auto read_x = [&](u4* x, int b, int q) {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            x[i] = *reinterpret_cast<const u4*>(lds + i * x_rows * x_stride + x_at + (b * kW4Block + q * 32) * 2);
-    };
-    auto fetch_x = [&](W4X<T>* x, int b, int q) {
-        const int k = b * kW4Block + q * 32 + quad * 8;
-        const uint32_t at = k < A.K ? (uint32_t)k * O::elem : kW4Far;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int h = 0; h < O::elem / 2; ++h)
-                x[r].v[h] = __builtin_bit_cast(
-                    u4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, (int)(row[r] + at), h * 16, 0));
-    };
+    // The blocks in registers: one is multiplied, the others are on their way.
+    constexpr int NB = !WHOLE ? 2 : CT == 4 ? 3 : 4;
+    Block block[NB];
+    fetch(block[0], wave);
 
-    auto pieces = [](const W4X<T>& x, u4* p) {
+    // x, as offsets in bytes from the tile's first row (with an index from x's)
+    const long long row0 = A.row_index ? 0 : tile.first;
+    __amdgpu_buffer_rsrc_t xbuf = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(static_cast<const char*>(A.x) + row0 * A.x_stride * O::elem), 0, (int)kW4Far, 0x00027000);
+    const int x_rows = min(tile.end - tile.first, TM);
+    auto row_at = [&](int m) -> uint32_t {
+        int src = tile.first + min(m, x_rows - 1);
+        if (A.row_index) src = A.row_index[src];
+        const bool bad = A.row_index && (src < 0 || src >= A.x_rows);
+        return m >= x_rows || bad ? kW4Far : (uint32_t)((src - (int)row0) * A.x_stride * O::elem);
+    };
+    for (int m = threadIdx.x; m < x_rows; m += blockDim.x) s_bad[m] = row_at(m) == kW4Far;
+    auto pieces = [](const u4* x, u4* p) {
         if constexpr (T == DQ_F32) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x.v[i / 4][i % 4]);
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[i / 4][i % 4]);
             split3(v, &p[0], &p[1], &p[2]);
         } else {
-            p[0] = x.v[0];
+            p[0] = x[0];
         }
     };
-    fv acc[CT][RT] = {};
-    const u4 ones = {O::kOnes, O::kOnes, O::kOnes, O::kOnes};
-    // Blocks ahead of the codes; steps ahead of x (in LDS it is one step away). Past the
-    // end the last block again: in bounds, not used.
-    constexpr int D = !XL ? 1 : CT == 4 ? 2 : 3;
-    constexpr int XR = XL ? 2 : RT * CT * O::elem <= 24 ? 4 : 2;
-    const int last = A.blocks - 1;
-    Block ahead[D];
-    W4X<T> x_ring[XL ? 1 : XR][RT];
-    u4 x_lds[2][P];
+    // whole rows: [P][rows][K padded, and 64 bytes], so that the rows of an operand begin in
+    // different banks; a lane without a row reads another's (not stored)
+    const int x_stride = A.blocks * (kW4Block * 2) + 64;
+    const int x_at = min(c >> 2, x_rows - 1) * x_stride + quad * 16;
+    // rings: a load takes 1024 bytes of half rows, lane by lane; piece i of 16 bytes of
+    // row m lies at i ^ (m / 2 % 8) (rows of 256 bytes: i ^ (m % 16)), so that 16 rows'
+    // pieces lie in different banks
+    constexpr int kLanes = kHalfRow / 16, kLoads = WHOLE ? 1 : kHalf / 1024;
+    constexpr int kSwizzle = O::elem == 2 ? 1 : 0;
+    uint32_t x_row[kLoads];
+    int x_k[kLoads];  // of the half block's 64, this lane's first
+    if constexpr (!WHOLE)
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(ahead[d], min(wave + d * waves, last));
-    if constexpr (XL) {
+        for (int d = 0; d < kLoads; ++d) {
+            const int m = d * (64 / kLanes) + lane / kLanes;
+            const int piece = lane % kLanes ^ (m >> kSwizzle) % kLanes;
+            x_row[d] = row_at(m) + piece * 16;
+            x_k[d] = piece * (16 / O::elem);
+        }
+    issue_fence();
+    char* const half0 = ring0 + wave * kHalf;
+    char* const half1 = ring1 + wave * kHalf;
+    auto fetch_x = [&](int at, int h) {
+        const int k0 = min(at, last) * kW4Block + h * 64;
+#pragma unroll
+        for (int d = 0; d < kLoads; ++d)
+            buffer16_to_lds(xbuf, (h ? half1 : half0) + d * 1024, x_k[d] < A.K - k0 ? x_row[d] : kW4Far, k0 * O::elem);
+    };
+    if constexpr (WHOLE) {
         const uint32_t items = (uint32_t)x_rows * A.per_row.d;  // of 8 elements
         for (uint32_t i = threadIdx.x; i < items; i += blockDim.x) {
             const uint32_t m = fdiv(i, A.per_row), k = (i - m * A.per_row.d) * 8;
-            int src = tile.first + (int)m;
-            if (A.row_index) src = A.row_index[src];
-            const bool bad = A.row_index && (src < 0 || src >= A.x_rows);
-            const uint32_t at = bad || (int)k >= A.K ? kW4Far : (uint32_t)((src - (int)row0) * A.x_stride + k) * O::elem;
-            W4X<T> x;
+            const uint32_t at = (int)k >= A.K ? kW4Far : row_at((int)m) + k * O::elem;
+            u4 x[O::elem / 2], p[P];
 #pragma unroll
             for (int h = 0; h < O::elem / 2; ++h)
-                x.v[h] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, (int)at, h * 16, 0));
-            u4 p[P];
+                x[h] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, (int)at, h * 16, 0));
             pieces(x, p);
 #pragma unroll
             for (int j = 0; j < P; ++j) *reinterpret_cast<u4*>(lds + (j * x_rows + (int)m) * x_stride + k * 2) = p[j];
         }
-        __syncthreads();
-        read_x(x_lds[0], min(wave, last), 0);
     } else {
-#pragma unroll
-        for (int q = 0; q < XR; ++q) fetch_x(x_ring[q], min(wave, last), q);
+        fetch_x(wave, 0);
+        fetch_x(wave, 1);
     }
-    for (int b = wave; b < A.blocks; b += waves) {
-        const Block now = ahead[0];
-        const int nb = min(b + waves, last);
+    issue_fence();
 #pragma unroll
-        for (int d = 0; d + 1 < D; ++d) ahead[d] = ahead[d + 1];
-        fetch(ahead[D - 1], min(b + D * waves, last));
+    for (int d = 1; d < NB; ++d) fetch(block[d], wave + d * waves);
+    issue_fence();
+    if constexpr (WHOLE) __syncthreads();
+
+    fv acc[CT][RT] = {};
+    const u4 ones = {O::kOnes, O::kOnes, O::kOnes, O::kOnes};
+    auto multiply = [&](Block& now, int b) {
         f4 sum[CT][RT], xs[RT];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            // this half of x has come when no more are on their way than the loads behind
+            // it: the other half's, and the next block's codes and scales
+            if constexpr (!WHOLE)
+                if (q % 2 == 0) {
+                    wait_vmcnt<kLoads + 2 * CT>();
+                    issue_fence();
+                }
             __builtin_amdgcn_sched_barrier(0);  // one step's operands in registers at a time
-            if (q % (4 / S) == 0) {
+            if (q % (4 / S) == 0)
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     xs[r] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int j = 0; j < CT; ++j) sum[j][r] = f4{0.0f, 0.0f, 0.0f, 0.0f};
                 }
-            }
             u4 w[CT];
 #pragma unroll
             for (int j = 0; j < CT; ++j) w[j] = O::codes(now.code[j][q]);
-            if constexpr (XL) read_x(x_lds[(q + 1) & 1], q < 3 ? b : nb, (q + 1) & 3);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 u4 p[P];
-                if constexpr (XL) {
+                if constexpr (WHOLE) {
 #pragma unroll
-                    for (int i = 0; i < P; ++i) p[i] = x_lds[q & 1][i];
+                    for (int i = 0; i < P; ++i)
+                        p[i] = *reinterpret_cast<const u4*>(lds + i * x_rows * x_stride + x_at + (b * kW4Block + q * 32) * 2);
                 } else {
-                    pieces(x_ring[q % XR][r], p);
+                    u4 x[O::elem / 2];
+                    const int first = (q % 2) * (kLanes / 2) + quad * (O::elem / 2);
+#pragma unroll
+                    for (int h = 0; h < O::elem / 2; ++h)
+                        x[h] = *reinterpret_cast<const u4*>((q < 2 ? half0 : half1) + (r * 16 + c) * kHalfRow +
+                                                            (((first + h) ^ (c >> kSwizzle) % kLanes) * 16));
+                    pieces(x, p);
                 }
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
@@ -198,40 +214,62 @@ __global__ void __launch_bounds__(RT * CT >= 3 ? 512 : 1024) k_w4_rows(W4Args A)
                     for (int j = 0; j < CT; ++j) sum[j][r] = O::mfma(p[i], w[j], sum[j][r]);
                 }
             }
-            if constexpr (!XL)
-                if (q & 1) {
-                    fetch_x(x_ring[(q - 1) % XR], q - 1 + XR < 4 ? b : nb, (q - 1 + XR) & 3);
-                    fetch_x(x_ring[q % XR], q + XR < 4 ? b : nb, (q + XR) & 3);
-                }
             if ((q + 1) % (4 / S) == 0) {
                 constexpr int per = 4 / S;
                 const int g = q / per;
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
                     const float sc = w4_scale_word<ST>(now.scale[j], g);
-                    const float z = (float)(now.zero[j] >> (8 * g) & 255u);
+                    const float z = (float)((now.zero[j] | z_default) >> (8 * g) & 255u);
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            acc[j][r][v] = __builtin_fmaf(sc, __builtin_fmaf(-z, xs[r][v], sum[j][r][v]), acc[j][r][v]);
+                        for (int v = 0; v < V; ++v) {
+                            float u = __builtin_fmaf(sc, __builtin_fmaf(-z, xs[r][v], sum[j][r][v]), acc[j][r][v]);
+                            // due here: the compiler would add in the next step, and keep the sums until then
+                            asm volatile("" : "+v"(u));
+                            acc[j][r][v] = u;
+                        }
                 }
             }
+            // the half that has been read is filled with the wave's next block's
+            if constexpr (!WHOLE)
+                if (q % 2 == 1) {
+                    wave_lds_fence();
+                    fetch_x(b + waves, q / 2);
+                    issue_fence();
+                }
         }
-    }
-
-    if constexpr (XL) __syncthreads();  // nobody reads x any more
-    fv* part = reinterpret_cast<fv*>(lds);
+        fetch(now, b + NB * waves);
+        issue_fence();
+    };
+    // left at once behind the last block: a way round the others back to the loop's
+    // head would cost every turn the waits of the shortest one
+    if (wave < A.blocks)
+        for (int b = wave;;) {
+#pragma unroll
+            for (int d = 0; d < NB; ++d) {
+                multiply(block[d], b);
+                b += waves;
+                if (b >= A.blocks) goto multiplied;
+            }
+        }
+multiplied:
+    if constexpr (!WHOLE) wait_vmcnt<0>();  // nothing is on its way to LDS any more
+    __syncthreads();                        // and nobody reads x
+    char* const parts_at = WHOLE ? lds : ring0;
+    constexpr int kParts = WHOLE ? 64 << 10 : kRing;  // bytes there
+    fv* part = reinterpret_cast<fv*>(parts_at);
     auto put = [&](int w) {
 #pragma unroll
         for (int j = 0; j < CT; ++j)
 #pragma unroll
             for (int r = 0; r < RT; ++r) part[(w * (CT * RT) + j * RT + r) * 64 + lane] = acc[j][r];
     };
-    // more than 64 KiB of parts: the upper half of the waves first hand theirs
-    // to the lower half
+    // more parts than fit: the upper half of the waves first hand theirs to the lower half
+    static_assert(WHOLE || w4_rows_waves<T, RT, CT, V>() / 2 * CT * RT * 256 * V <= kRing, "half of the parts fit");
     int parts = waves;
-    if (waves * CT * RT > 64) {
+    if (waves * CT * RT * (256 * V) > kParts) {
         parts = waves / 2;
         if (wave >= parts) put(wave - parts);
         __syncthreads();

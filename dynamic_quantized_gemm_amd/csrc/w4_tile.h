@@ -145,9 +145,8 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
         // stage_k: the element of a row at which the stage's 128 begin
 #pragma unroll
         for (int i = 0; i < CPW; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                xbuf, (__attribute__((address_space(3))) void*)(dst + (wave * CPW + i) * 1024), 16,
-                (int)voff[i % NV], (int)((uint32_t)stage_k * 2 + (uint32_t)(i / NV * 16) * x_bytes), 0, 0);
+            buffer16_to_lds(xbuf, dst + (wave * CPW + i) * 1024, voff[i % NV],
+                            (uint32_t)stage_k * 2 + (uint32_t)(i / NV * 16) * x_bytes);
     };
     // the sums of x of thread t's row, as an offset (they take less than 2^32 bytes)
     uint32_t sum_at;

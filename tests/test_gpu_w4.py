@@ -285,3 +285,26 @@ def test_more_rows_than_are_prepared_at_once(gpu, type, K, rows):
     one = {n: v if n in ("x", "type", "scale", "N", "K", "group", "gated") else 1 if n == "experts" else v[:1]
            for n, v in c.items()}
     W.check(_forward(gpu, torch, one), *W.want(one, 0, c["x"]), "f32", "one expert")
+
+
+@pytest.mark.parametrize("type", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows", [3, 16, 30, 44, 60, 200])
+def test_what_the_chip_held_before_does_not_show(gpu, type, rows):
+    """A K that ends inside a block and rows that end inside a tile, behind a
+    call whose x was all NaN: what it left in the compute units' memory is not
+    multiplied."""
+    import torch
+
+    c = W.make(torch, rows, 1, 4096, 168, 128, rows, type, bias=False)
+    bad = W.make(torch, rows, 1, 4096, 2048, 128, 256, type, bias=False)
+    hb, h = W.handle(gpu, bad, "f32", 256), W.handle(gpu, c, "f32", 256)
+    x, nan = c["x"].cuda(), torch.full((256, 2048), float("nan"), dtype=c["x"].dtype, device="cuda")
+    out, junk = torch.empty((rows, 4096), device="cuda"), torch.empty((256, 4096), device="cuda")
+    ref, bound = W.want(c, 0, c["x"])
+    for n in (256, 64, 48, 16, 2):
+        gpu.dq_w4_forward(hb, nan[:n], junk[:n])
+        gpu.dq_w4_forward(h, x, out)
+        torch.cuda.synchronize()
+        W.check(out, ref, bound, "f32", f"behind {n} rows of NaN")
+    gpu.dq_w4_release(hb)
+    gpu.dq_w4_release(h)
