@@ -43,6 +43,7 @@ struct RouteArgs {
     int32_t* before;   // [chunks][words * 4]: its rows in earlier chunks
     int32_t* totals;   // [words * 4]
     int tokens, experts, top_k, chunks, words, type, sigmoid, normalize;
+    int vec;  // a lane's neighbouring logits can be loaded at once
     float scale;
 };
 
@@ -125,16 +126,17 @@ __device__ __forceinline__ void first_rows(const int* s_total, int* s_first, int
 // experts, top 8: see the figures below. A chunk's ranks come from a 64-bit mask of
 // tokens for each expert, so they do not depend on the order of the atomics. One
 // chunk alone is finished here.
-template <int V, int L>
+// V: logits of a lane; KEEP: how many of them, sorted, the rounds can need.
+template <int V, int KEEP, int L>
 __global__ void __launch_bounds__(1024) k_moe_choose(RouteArgs A) {
     __shared__ u64 s_mask[DQ_MOE_EXPERTS_MAX];
     __shared__ int s_total[DQ_MOE_EXPERTS_MAX], s_first[DQ_MOE_EXPERTS_MAX + 1], s_wave[16];
     constexpr int kAtOnce = 1024 / L;          // tokens of the workgroup
     constexpr int kSlots = L == 16 ? 2 : 1;    // choices that a lane keeps
+    constexpr int kTurns = kChunk / kAtOnce > 0 ? kChunk / kAtOnce : 1;
     const int l = threadIdx.x % L;
     for (int e = threadIdx.x; e < A.words * 4; e += 1024) s_mask[e] = 0;
     __syncthreads();
-    constexpr int kTurns = kChunk / kAtOnce > 0 ? kChunk / kAtOnce : 1;
     int id[kTurns][kSlots];
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
@@ -144,12 +146,38 @@ __global__ void __launch_bounds__(1024) k_moe_choose(RouteArgs A) {
         const long long at = (some ? t : A.tokens - 1) * A.stride;
         u64 key[V];
         bool nan = false;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * L + l;
-            const float v = load1(A.logits, at + min(e, A.experts - 1), A.type);
+        auto take = [&](int i, int e, float v) {
             key[i] = e < A.experts ? route_key(v, e) : kNoKey;
             nan |= e < A.experts && v != v;
+        };
+        // which lane has which logit does not matter: a key carries its expert
+        if (A.vec && A.type == DQ_F32) {
+            constexpr int W = V < 4 ? V : 4;
+            typedef float fw __attribute__((ext_vector_type(W)));
+#pragma unroll
+            for (int i = 0; i < V; i += W) {
+                const int e = i * L + l * W;
+                const fw v = *reinterpret_cast<const fw*>(static_cast<const float*>(A.logits) + at + min(e, A.experts - W));
+#pragma unroll
+                for (int k = 0; k < W; ++k) take(i + k, e + k, v[k]);
+            }
+        } else if (A.vec) {
+            constexpr int W = V < 8 ? V : 8;
+            typedef uint16_t hw __attribute__((ext_vector_type(W)));
+#pragma unroll
+            for (int i = 0; i < V; i += W) {
+                const int e = i * L + l * W;
+                const hw v = *reinterpret_cast<const hw*>(static_cast<const uint16_t*>(A.logits) + at + min(e, A.experts - W));
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    take(i + k, e + k, A.type == DQ_BF16 ? bf16_bits_to_f32(v[k]) : (float)__builtin_bit_cast(_Float16, (uint16_t)v[k]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = i * L + l;
+                take(i, e, load1(A.logits, at + min(e, A.experts - 1), A.type));
+            }
         }
         // Batcher's odd-even merge sort, falling
 #pragma unroll
@@ -177,8 +205,8 @@ __global__ void __launch_bounds__(1024) k_moe_choose(RouteArgs A) {
                 if (l + s * L == j) won[s] = best;
             if (key[0] == best) {
 #pragma unroll
-                for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-                key[V - 1] = kNoKey;
+                for (int i = 0; i + 1 < KEEP; ++i) key[i] = key[i + 1];
+                key[KEEP - 1] = kNoKey;
             }
         }
         float part[kSlots], sum = 0.0f;
@@ -271,12 +299,21 @@ __global__ void __launch_bounds__(1024) k_moe_place(RouteArgs A) {
         const int runs = 1024 / A.words, w = threadIdx.x % A.words, run = threadIdx.x / A.words;
         if (run < runs) {
             int before[4] = {}, total[4] = {};
-            for (int c = run; c < A.chunks; c += runs) {
-                const uint32_t n = reinterpret_cast<const uint32_t*>(A.counts)[(size_t)c * A.words + w];
+            constexpr int J = 16;  // counts on their way at a time
+            for (int c = run; c < A.chunks; c += J * runs) {
+                uint32_t n[J];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    total[i] += n >> (8 * i) & 255;
-                    before[i] += c < c0 ? n >> (8 * i) & 255 : 0;
+                for (int j = 0; j < J; ++j)
+                    n[j] = reinterpret_cast<const uint32_t*>(A.counts)[(size_t)min(c + j * runs, A.chunks - 1) * A.words + w];
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int cj = c + j * runs;
+                    if (cj >= A.chunks) n[j] = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        total[i] += n[j] >> (8 * i) & 255;
+                        before[i] += cj < c0 ? n[j] >> (8 * i) & 255 : 0;
+                    }
                 }
             }
 #pragma unroll
@@ -432,13 +469,16 @@ void launch_combine(dq_dtype to, const CombineArgs& A, bool vec, hipStream_t s) 
 
 void launch_choose(const RouteArgs& A, hipStream_t s) {
     const dim3 grid((unsigned)A.chunks), block(1024);
-    // 16 lanes a token, up to 16 logits each; more lanes beyond that
-    if (A.experts <= 32) hipLaunchKernelGGL((k_moe_choose<2, 16>), grid, block, 0, s, A);
-    else if (A.experts <= 64) hipLaunchKernelGGL((k_moe_choose<4, 16>), grid, block, 0, s, A);
-    else if (A.experts <= 128) hipLaunchKernelGGL((k_moe_choose<8, 16>), grid, block, 0, s, A);
-    else if (A.experts <= 256) hipLaunchKernelGGL((k_moe_choose<16, 16>), grid, block, 0, s, A);
-    else if (A.experts <= 512) hipLaunchKernelGGL((k_moe_choose<16, 32>), grid, block, 0, s, A);
-    else hipLaunchKernelGGL((k_moe_choose<16, 64>), grid, block, 0, s, A);
+    // 16 lanes a token, up to 16 logits each; more lanes beyond that. Of a lane's sorted
+    // logits up to 8 choices can need the first 8
+    const bool few = A.top_k <= 8;
+    if (A.experts <= 32) hipLaunchKernelGGL((k_moe_choose<2, 2, 16>), grid, block, 0, s, A);
+    else if (A.experts <= 64) hipLaunchKernelGGL((k_moe_choose<4, 4, 16>), grid, block, 0, s, A);
+    else if (A.experts <= 128) hipLaunchKernelGGL((k_moe_choose<8, 8, 16>), grid, block, 0, s, A);
+    else if (A.experts <= 256 && few) hipLaunchKernelGGL((k_moe_choose<16, 8, 16>), grid, block, 0, s, A);
+    else if (A.experts <= 256) hipLaunchKernelGGL((k_moe_choose<16, 16, 16>), grid, block, 0, s, A);
+    else if (A.experts <= 512) hipLaunchKernelGGL((k_moe_choose<16, 16, 32>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((k_moe_choose<16, 16, 64>), grid, block, 0, s, A);
 }
 
 size_t float_bytes(int type) { return type == DQ_F32 ? 4 : 2; }
@@ -523,6 +563,9 @@ extern "C" int dq_moe_route(dq_moe_ctx* ctx, int64_t tokens, const void* logits,
     A.sigmoid = ctx->scoring == DQ_MOE_SIGMOID;
     A.normalize = ctx->normalize;
     A.scale = ctx->scale;
+    // as many logits as a lane takes at a time divide the experts, and rows begin at 16 bytes
+    const int wide = ctx->experts <= 32 ? 2 : ctx->experts <= 64 ? 4 : 8;
+    A.vec = (uintptr_t)logits % 16 == 0 && logits_stride * float_bytes(ctx->logits_type) % 16 == 0 && ctx->experts % wide == 0;
     const hipStream_t s = (hipStream_t)stream;
     if (tokens == 0) {
         hipLaunchKernelGGL(k_moe_none, dim3(1), dim3(256), 0, s, offsets, ctx->experts);

@@ -232,9 +232,8 @@ int launch_tile(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
         }
         T.row_lo = (int)lo;
         T.row_hi = (int)hi;
-        const int wide = 2;
         const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
-        T.tiles_n = (used + 4 * wide - 1) / (4 * wide);
+        T.tiles_n = (used + 7) / 8;
         const int64_t rows = hi - lo;
         const int64_t tiles_m = A.offsets ? rows / kW4TileRows + std::min<int64_t>(rows, c->experts)
                                           : (rows + kW4TileRows - 1) / kW4TileRows;
@@ -248,15 +247,22 @@ int launch_tile(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
         const int64_t grid = (units() + 7) / 8 * 8 * T.gm * T.gn;
         if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
         T.vec_store = (uintptr_t)A.y % 16 == 0 && c->N % 8 == 0;
-        hipLaunchKernelGGL(k.tile(c->S, c->scale_type, A.row_index && !T.x_by_row), dim3((unsigned)grid), dim3(128 * wide), 0, s, T);
+        hipLaunchKernelGGL(k.tile(c->S, c->scale_type, A.row_index && !T.x_by_row), dim3((unsigned)grid), dim3(256), 0, s, T);
         DQ_LAUNCH_CHECK("product with 4-bit weights");
     }
     return DQ_OK;
 }
 
+// Many rows, where an expert has more than a tile of the other kernel's (kTileMean) and there
+// are tiles of 128 x 128 for three quarters of the chip: a tile takes its time
+// whatever the others do, and few of them leave the rest idle. 4096 x 4096, us
+// (this one / the other): 512 rows (128 tiles) 51.8 / 44.0, 1024 rows 53.9 / 84.1;
+// 16384 x 4096: 128 rows (128 tiles) 72.2 / 44.7, 256 rows 72.1 / 86.0.
 int launch(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
     const int mean = A.offsets ? (A.rows + c->experts - 1) / c->experts : A.rows;
-    if (mean > kTileMean && c->copy_rows) return launch_tile(c, A, s);
+    const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
+    const int64_t tiles = (int64_t)((A.rows + kW4TileRows - 1) / kW4TileRows) * ((used + 7) / 8);
+    if (mean > kTileMean && tiles * 4 > c->cus * 3 && c->copy_rows) return launch_tile(c, A, s);
     return launch_rows(c, A, s);
 }
 
