@@ -257,12 +257,13 @@ int launch_tile(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
 // are tiles of 128 x 128 for three quarters of the chip: a tile takes its time
 // whatever the others do, and few of them leave the rest idle. 4096 x 4096, us
 // (this one / the other): 512 rows (128 tiles) 51.8 / 44.0, 1024 rows 53.9 / 84.1;
-// 16384 x 4096: 128 rows (128 tiles) 72.2 / 44.7, 256 rows 72.1 / 86.0.
+// 16384 x 4096: 128 rows (128 tiles) 72.2 / 44.7, 256 rows 72.1 / 86.0. Rows that
+// do not lie 16 bytes apart go there from the same rows on: it copies them first.
 int launch(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
     const int mean = A.offsets ? (A.rows + c->experts - 1) / c->experts : A.rows;
     const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
     const int64_t tiles = (int64_t)((A.rows + kW4TileRows - 1) / kW4TileRows) * ((used + 7) / 8);
-    if (mean > kTileMean && tiles * 4 > c->cus * 3 && c->copy_rows) return launch_tile(c, A, s);
+    if (mean > kTileMean && (tiles * 4 > c->cus * 3 || !A.vec) && c->copy_rows) return launch_tile(c, A, s);
     return launch_rows(c, A, s);
 }
 
