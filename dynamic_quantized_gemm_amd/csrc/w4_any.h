@@ -1,7 +1,7 @@
 // w4_any.h -- the kernel of products with 4-bit weights for few rows that
 // w4_rows.h cannot take: rows that do not start 16 bytes apart, a K that
 // does not end there, offsets beyond 31 bits. The same arithmetic, with x read
-// element by element and from 64-bit addresses.
+// from 64-bit addresses of any alignment, and the end of a row element by element.
 #pragma once
 
 #include "w4_device.h"

@@ -100,6 +100,8 @@ __device__ __forceinline__ void w4_load8(const char* row, int k, int K, bool vec
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[4 * h + i] = t[i];
             }
+        } else if (k + 8 <= K) {  // loads of 16 bytes from any address
+            __builtin_memcpy(v, p, 32);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = k + i < K ? reinterpret_cast<const float*>(p)[i] : 0.0f;
@@ -109,6 +111,8 @@ __device__ __forceinline__ void w4_load8(const char* row, int k, int K, bool vec
         u4 t = {0, 0, 0, 0};
         if (k < K) t = *reinterpret_cast<const u4*>(p);
         out[0] = t;
+    } else if (k + 8 <= K) {
+        __builtin_memcpy(out, p, 16);
     } else {
         unsigned v[8];
 #pragma unroll
