@@ -122,10 +122,13 @@ __device__ __forceinline__ void first_rows(const int* s_total, int* s_first, int
 
 // The choice for a chunk of tokens. L lanes take a token, each V of its logits
 // as sorted keys; every round takes the largest first key among the lanes and
-// out of its lane. Bound by these rounds' dependent steps: 16001 tokens of 256
-// experts, top 8: see the figures below. A chunk's ranks come from a 64-bit mask of
-// tokens for each expert, so they do not depend on the order of the atomics. One
-// chunk alone is finished here.
+// out of its lane. Bound by these rounds' dependent steps (four moves across lanes
+// and maxima, then the shift): 16001 tokens of 256 experts in bf16, top 8, 8.3 us,
+// of which the 8 MB of logits would take 1.3. With a wave a token, a maximum and
+// its index as two values each, it was most of 257 us together with one
+// workgroup's sums. A chunk's ranks come from a 64-bit mask of tokens for each
+// expert, so they do not depend on the order of the atomics. One chunk alone is
+// finished here: 8 tokens of 64 experts take one launch of 4.9 us, not two.
 // V: logits of a lane; KEEP: how many of them, sorted, the rounds can need.
 template <int V, int KEEP, int L>
 __global__ void __launch_bounds__(1024) k_moe_choose(RouteArgs A) {
@@ -285,7 +288,9 @@ __global__ void __launch_bounds__(1024) k_moe_scan(RouteArgs A) {
 }
 
 // The rows of kPlace chunks: what their tokens' ranks begin at. Up to
-// kScanChunks chunks, every workgroup sums all of their counts by itself.
+// kScanChunks chunks, every workgroup sums all of their counts by itself (251
+// chunks of 256 experts: 64 KB from the L2, 7.7 us in all, where a scan of one
+// workgroup between two launches took some 200).
 __global__ void __launch_bounds__(1024) k_moe_place(RouteArgs A) {
     __shared__ int s_total[DQ_MOE_EXPERTS_MAX], s_before[kPlace][DQ_MOE_EXPERTS_MAX];
     __shared__ int s_first[DQ_MOE_EXPERTS_MAX + 1], s_wave[16];
@@ -392,7 +397,9 @@ __device__ __forceinline__ void load_piece(const void* p, size_t i, float* v) {
 }
 
 // Bound by memory: each row of y is read once. A thread takes E elements of a
-// token, J of its rows on their way at a time.
+// token, J of its rows on their way at a time: 8101 tokens of 4 rows of 4096 in
+// fp32 with a bf16 sum, 664 MB, 116.8 us, 5.7 TB/s of what a copy reaches 6.2
+// (an element a thread: 310 us).
 template <int TY, int TO, int E>
 __global__ void __launch_bounds__(256) k_moe_combine(CombineArgs A) {
     const uint32_t item = blockIdx.x * 256u + threadIdx.x;

@@ -18,6 +18,12 @@
 // The sum of a group's x, which its zero point multiplies, is one more
 // product, with ones: in the accumulators' layout without any exchange, on
 // matrix cores that are idle most of the time here.
+//
+// One row of 16384 x 8192 in groups of 32 with zero points, fp16 (77.6 MB):
+// 17.5 to 18.6 us, 4.2 to 4.4 TB/s. A launch that does nothing but find its tile, ask for the
+// first blocks and store takes 3.4 to 5.5 us; the rest runs at 5.5 TB/s and
+// more. 48 gated rows of 16384 x 4096 (35.8 MB): 14.7 to 15.5 us, of which the
+// products of a wave of 48 x 64 are 3.2 and the vector operations about as much.
 #pragma once
 
 #include "w4_device.h"

@@ -799,8 +799,9 @@ void dq_kv_release(dq_kv_ctx* ctx);
  * and with gated != 0, where W has 2 N rows (N of a gate, then N of values),
  *   y[m, n] = silu(v) u,  v = row n's sum, u = row N + n's,
  *   silu(v) = v / (1 + exp(-v)).
- * Products are exact and sums fp32, the scale multiplies its group's sum, and
- * y is rounded once. A NaN or infinity in a row of x gives NaN or infinities in that
+ * Products of x and codes are exact and their sums fp32 (an error is relative to
+ * the sum of the magnitudes |s| (q + z) |x|), the scale multiplies its group's
+ * sum, and y is rounded once. A NaN or infinity in a row of x gives NaN or infinities in that
  * row of y and no other; so does one whose sums of code times x leave fp32.
  *
  * dq_w4_init: experts matrices of the same sizes (1: dq_w4_forward), each at
@@ -824,10 +825,13 @@ void dq_kv_release(dq_kv_ctx* ctx);
  * [experts + 1] on the device) are products with expert e's weights; row r of
  * y comes from row row_index[r] (int32 [rows] on the device; NULL: r) of x, which
  * has x_rows. Rows of y before offsets[0] and from the last offset on are left
- * as they were. An offset outside [0, rows] counts as the nearest end, one below
- * the one before it as that one (an expert has no rows then, and rows that two
- * experts claim get either's); a row_index outside [0, x_rows) gives a row of NaN.
+ * as they were. An offset outside [0, rows] counts as the nearest end; an expert
+ * whose rows end before they begin has none; a row that several experts claim
+ * gets one's result or is left. A row_index outside [0, x_rows) gives a row of NaN.
  * Both are asynchronous on `stream` and allocate nothing; zero rows is a no-op.
+ * They use the context's workspace: calls on one context must not overlap. A
+ * captured call keeps whether there were zero points and a bias: after a
+ * dq_w4_set_w that changes this it is captured again.
  * Errors: DQ_ERR_STATE (no context or weights, another device), DQ_ERR_ARG,
  * DQ_ERR_RANGE (beyond one launch), DQ_ERR_HIP.
  * ---------------------------------------------------------------------- */
@@ -878,8 +882,8 @@ void dq_w4_release(dq_w4_ctx* ctx);
  *
  * dq_moe_combine: out[t] = add[t] + sum_j weights[t, j] y[row_of[t, j]] for y
  * [rows, N], out and add (NULL: 0) [tokens, N], dense (DEVICE; y_type, out_type:
- * DQ_F32 / DQ_BF16 / DQ_F16; add has out's type and may be out), summed in fp32
- * in the order of j and rounded once. A row_of below 0 adds nothing whatever its
+ * DQ_F32 / DQ_BF16 / DQ_F16; add has out's type and may be out; y may not overlap
+ * out), summed in fp32 in the order of j and rounded once. A row_of below 0 adds nothing whatever its
  * weight, one of rows or more gives NaN. It needs no workspace: calls may overlap.
  *
  * Both are asynchronous on `stream` and allocate nothing. dq_moe_route uses the

@@ -308,3 +308,79 @@ def test_what_the_chip_held_before_does_not_show(gpu, type, rows):
         W.check(out, ref, bound, "f32", f"behind {n} rows of NaN")
     gpu.dq_w4_release(hb)
     gpu.dq_w4_release(h)
+
+
+def test_refusals_with_a_context(gpu):
+    """What a call refuses leaves y as it was."""
+    import ctypes as C
+
+    import torch
+
+    lib = gpu.load()
+    c = W.make(torch, 1, 2, 24, 64, 32, 10)
+    h = gpu.dq_w4_init(2, 24, 64, 32, gpu.DQ_BF16, gpu.DQ_BF16, gpu.DQ_F32, False, 10)
+    x, y = c["x"].cuda(), torch.full((10, 24), 5.0, device="cuda")
+    off = torch.tensor([0, 4, 10], dtype=torch.int32, device="cuda")
+
+    def refused(status, call):
+        with pytest.raises(gpu.DQError) as e:
+            call()
+        assert e.value.status == status, e.value
+        torch.cuda.synchronize()
+        assert (y == 5.0).all()
+
+    refused(gpu.DQ_ERR_STATE, lambda: gpu.dq_w4_forward_grouped(h, x, off, y))  # no weights yet
+    gpu.dq_w4_set_w(h, *[None if c[n] is None else c[n].cuda() for n in ("codes", "scales", "zeros", "bias")])
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward(h, x, y))  # several experts
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x, off[:2].contiguous(), y))
+    refused(gpu.DQ_ERR_TYPE, lambda: gpu.dq_w4_forward_grouped(h, x.float(), off, y))
+    refused(gpu.DQ_ERR_TYPE, lambda: gpu.dq_w4_forward_grouped(h, x, off.long(), y))
+    refused(gpu.DQ_ERR_TYPE, lambda: gpu.dq_w4_forward_grouped(h, x, off, y.bfloat16()))
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x[:, :63], off, y))
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x.t().contiguous().t(), off, y))
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x, off, y.t().contiguous().t()))
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x[:9], off, y))  # rows of x that are not there
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x, off, y, row_index=off))  # too short
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_w4_forward_grouped(h, x, off, torch.empty((11, 24), device="cuda")))
+    p, q = x.data_ptr(), y.data_ptr()
+    st = torch.cuda.current_stream().cuda_stream
+    assert lib.dq_w4_forward_grouped(h, 10, off.data_ptr(), 10, p + 1, 64, None, q, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_forward_grouped(h, 10, off.data_ptr() + 2, 10, p, 64, None, q, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_forward_grouped(h, 10, off.data_ptr(), 10, p, 64, None, q + 2, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_forward_grouped(h, 10, off.data_ptr(), 10, p, -64, None, q, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_forward_grouped(h, 10, None, 10, p, 64, None, q, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_forward_grouped(h, 10, off.data_ptr(), 0, p, 64, None, q, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_forward_grouped(h, -1, off.data_ptr(), 10, p, 64, None, q, st) == gpu.DQ_ERR_ARG
+    assert lib.dq_w4_set_w(h, None, p, None, None, st) == gpu.DQ_ERR_ARG
+    torch.cuda.synchronize()
+    assert (y == 5.0).all()
+    m = gpu.dq_moe_init(4, 8, 2, gpu.DQ_F32)
+    l, i, w = torch.zeros((5, 8), device="cuda"), torch.zeros((5, 2), dtype=torch.int32, device="cuda"), torch.zeros((5, 2), device="cuda")
+    o = torch.zeros(9, dtype=torch.int32, device="cuda")
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_moe_route(m, l, i, w, o, i, i))  # five tokens
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_moe_route(m, l[:4], i, w, o[:8].contiguous(), i, i))
+    refused(gpu.DQ_ERR_TYPE, lambda: gpu.dq_moe_route(m, l[:4].half(), i, w, o, i, i))
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_moe_combine(m, y, w, i, torch.empty((5, 24), device="cuda")))
+    refused(gpu.DQ_ERR_ARG, lambda: gpu.dq_moe_combine(m, y, w, i, torch.empty((4, 20), device="cuda")))
+    refused(gpu.DQ_ERR_TYPE, lambda: gpu.dq_moe_combine(m, y, w, i, y[:4], add=y[:4].half()))
+    gpu.dq_moe_release(m)
+    gpu.dq_w4_release(h)
+
+
+def test_two_contexts_on_two_streams(gpu):
+    """Calls that overlap, each on a context of its own, as alone."""
+    import torch
+
+    cases = [W.make(torch, i, 1, 200, 900, 64, 120, "bf16") for i in range(2)]
+    hs = [W.handle(gpu, c, "f32", 120) for c in cases]
+    xs = [c["x"].cuda() for c in cases]
+    outs = [torch.empty((120, 200), device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for h, x, o, s in zip(hs, xs, outs, streams):
+            gpu.dq_w4_forward(h, x, o, stream=s)
+    torch.cuda.synchronize()
+    for c, o, h in zip(cases, outs, hs):
+        W.check(o, *W.want(c, 0, c["x"]), "f32", "overlapping")
+        gpu.dq_w4_release(h)
