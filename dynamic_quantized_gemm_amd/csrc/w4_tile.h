@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(256, 2) k_w4_tile(W4TileArgs A) {
     // One stage: 4 steps of 32 k, each 16 products of a wave, column by column: a
     // column's operand is free after its 4, and the next step's is unpacked into it
     // while the next column's run; behind a group's last step its sums are scaled and
-    // added likewise. The scheduling groups put these between the products.
+    // added likewise. (Named scheduling groups, a raised wave priority and codes
+    // fetched half a stage earlier or later made no difference.)
     u4 w[4];
 #pragma unroll
     for (int n = 0; n < 4; ++n) w[n] = O::codes(code[0][n][0]);
@@ -265,15 +266,6 @@ __global__ void __launch_bounds__(256, 2) k_w4_tile(W4TileArgs A) {
                         for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(s, t[m][n][v], acc[m][n][v]);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 4 * kW4TileM; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);                 // a product
-                if (k < 2 * kW4TileM) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // an LDS read
-                if (k >= kW4TileM) {                                                    // vector operations
-                    if (ends) __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
-                    else __builtin_amdgcn_sched_group_barrier(0x2, 2, 0);
-                }
-            }
             // results are due here: left to itself the compiler moves the additions into the
             // next stage, and keeps every group's sums until then
 #pragma unroll
@@ -295,41 +287,67 @@ __global__ void __launch_bounds__(256, 2) k_w4_tile(W4TileArgs A) {
     lds_barrier();  // nobody reads a stage any more, nothing is on its way to one
 
     // what is left of the zero points: (z - 8) s of 32 groups at a time against
-    // the sums of x, which are there times -8
+    // the sums of x, which are there times -8. All is asked for before the first is
+    // used
     if (a.zeros) {
         const int groups = a.blocks * S;
+        const uint8_t* zeros = a.zeros + base * a.blocks * (16 * S);
+        uint32_t x_at[kW4TileM];
+#pragma unroll
+        for (int m = 0; m < kW4TileM; ++m) {
+            const int r = min(tile.first + wm * (16 * kW4TileM) + m * 16 + c, last);
+            int src = A.by_row ? r - A.row_lo : r;
+            if (!A.by_row && a.row_index) {
+                src = a.row_index[r];
+                if (src < 0 || src >= a.x_rows) src = 0;
+            }
+            x_at[m] = (uint32_t)src * (uint32_t)groups;
+        }
         for (int g0 = 0; g0 < groups; g0 += 32) {
+            uint32_t s_raw[4][8], z_raw[4][8];
+            float x_sum[kW4TileM][8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int g = min(g0 + quad * 8 + k, groups - 1);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const uint32_t at = (uint32_t)(((n * a.blocks + g / S) * 16 + c) * S + g % S);
+                    if constexpr (SB == 4) s_raw[n][k] = reinterpret_cast<const uint32_t*>(scales)[at];
+                    else s_raw[n][k] = reinterpret_cast<const uint16_t*>(scales)[at];
+                    z_raw[n][k] = zeros[at];
+                }
+            }
+            // a lane's 8 sums at once: one by one each of a load's lanes is an access of its own
+#pragma unroll
+            for (int m = 0; m < kW4TileM; ++m) {
+                const int g = g0 + quad * 8;
+                const float* p = A.sums + x_at[m];
+                if (g + 8 <= groups) {
+                    __builtin_memcpy(x_sum[m], p + g, 32);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x_sum[m][k] = p[min(g + k, groups - 1)];
+                }
+            }
+            issue_fence();
             u4 zs[4][3];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 float v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int g = min(g0 + quad * 8 + k, groups - 1), b = g / S;
-                    const size_t at = (((base + n) * a.blocks + b) * 16 + c) * S + g % S;
+                for (int k = 0; k < 8; ++k)
                     v[k] = g0 + quad * 8 + k < groups
-                               ? w4_scale(a.scales, at, a.scale_type) * (((float)a.zeros[at] - 8.0f) * 0.125f)
+                               ? w4_scale_word<ST>(&s_raw[n][k], 0) * (((float)z_raw[n][k] - 8.0f) * 0.125f)
                                : 0.0f;
-                }
                 split3(v, &zs[n][0], &zs[n][1], &zs[n][2]);
             }
 #pragma unroll
             for (int m = 0; m < kW4TileM; ++m) {
-                const int r = min(tile.first + wm * (16 * kW4TileM) + m * 16 + c, last);
-                int src = A.by_row ? r - A.row_lo : r;
-                if (!A.by_row && a.row_index) {
-                    src = a.row_index[r];
-                    if (src < 0 || src >= a.x_rows) src = 0;
-                }
-                const float* p = A.sums + (size_t)src * groups;
-                float v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int g = g0 + quad * 8 + k;
-                    v[k] = g < groups ? p[min(g, groups - 1)] : 0.0f;
-                }
+                for (int k = 0; k < 8; ++k)
+                    if (g0 + quad * 8 + k >= groups) x_sum[m][k] = 0.0f;
                 u4 xs[3];
-                split3(v, &xs[0], &xs[1], &xs[2]);
+                split3(x_sum[m], &xs[0], &xs[1], &xs[2]);
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
