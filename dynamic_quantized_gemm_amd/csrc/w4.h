@@ -11,7 +11,7 @@
 // Packed layout. The rows of W are taken 16 at a time (a tile: the columns of
 // one 16x16 block of y) and K 128 at a time (a block). With gated != 0 the
 // tiles alternate: 16 rows of the gate, the 16 rows of the values they gate.
-// Rows are padded to whole tiles (their number to a multiple of 8), K to whole
+// Rows are padded to whole tiles (their number to a multiple of 16), K to whole
 // blocks; what is padded has code, scale and zero point 0.
 //   codes  [experts][tiles][blocks][64 lanes][16 bytes]: a lane's 4 words are
 //          the 4 k-steps of 32, for row lane % 16 and k = 8 (lane / 16) + i of
@@ -28,7 +28,7 @@
 namespace dq {
 
 constexpr int kW4Block = 128;  // k of a block
-constexpr int kW4TilePad = 8;  // tiles of 16 rows are padded to a multiple of this
+constexpr int kW4TilePad = 16;  // tiles of 16 rows are padded to a multiple of this
 
 // the kernels' arguments; what they read has been checked against these sizes
 struct W4Args {
@@ -83,7 +83,7 @@ struct W4Prepare;
 struct W4Kernels {
     void (*(*rows)(int rows, int col_tiles, int S, int scales))(W4Args);
     void (*(*any)(int rows, int col_tiles, int S))(W4Args);
-    void (*(*tile)(int S, int scales, bool gather))(W4TileArgs);
+    void (*(*tile)(int wide, int S, int scales, bool gather))(W4TileArgs);
     void (*prepare)(W4Prepare);
 };
 W4Kernels w4_kernels_bf16();

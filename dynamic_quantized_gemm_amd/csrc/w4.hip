@@ -233,21 +233,24 @@ int launch_tile(const dq_w4_ctx* c, const W4Args& A, hipStream_t s) {
         T.row_lo = (int)lo;
         T.row_hi = (int)hi;
         const int used = (c->N + 15) / 16 * (c->gated ? 2 : 1);
-        T.tiles_n = (used + 7) / 8;
         const int64_t rows = hi - lo;
         const int64_t tiles_m = A.offsets ? rows / kW4TileRows + std::min<int64_t>(rows, c->experts)
                                           : (rows + kW4TileRows - 1) / kW4TileRows;
+        // 256 columns a workgroup where that leaves one for every compute unit, else 128
+        // (us of 256 / 128: 4096 rows of 4096 x 4096 154 / 161, 1024 rows 67 / 53)
+        const int wide = (rows + kW4TileRows - 1) / kW4TileRows * ((used + 15) / 16) >= c->cus ? 4 : 2;
+        T.tiles_n = (used + 4 * wide - 1) / (4 * wide);
         T.tiles_m = (int)tiles_m;
-        // units of 4 x 8 tiles to an XCD, smaller ones where there are few
+        // units of 4 x 4 tiles (of 256 columns, else 4 x 8) to an XCD, smaller ones where there are few
         T.gm = 4;
-        T.gn = 8;
+        T.gn = 16 / wide;
         auto units = [&] { return (tiles_m + T.gm - 1) / T.gm * ((T.tiles_n + T.gn - 1) / T.gn); };
         while (T.gn > 1 && units() < 32) T.gn /= 2;
         while (T.gm > 1 && units() < 32) T.gm /= 2;
         const int64_t grid = (units() + 7) / 8 * 8 * T.gm * T.gn;
         if (grid > INT32_MAX) DQ_FAIL(DQ_ERR_RANGE, "too many rows for one launch");
         T.vec_store = (uintptr_t)A.y % 16 == 0 && c->N % 8 == 0;
-        hipLaunchKernelGGL(k.tile(c->S, c->scale_type, A.row_index && !T.x_by_row), dim3((unsigned)grid), dim3(256), 0, s, T);
+        hipLaunchKernelGGL(k.tile(wide, c->S, c->scale_type, A.row_index && !T.x_by_row), dim3((unsigned)grid), dim3(128 * wide), 0, s, T);
         DQ_LAUNCH_CHECK("product with 4-bit weights");
     }
     return DQ_OK;

@@ -1,7 +1,7 @@
 // w4_tile.h -- the kernel of products with 4-bit weights for many rows.
 //
 // Bound by the matrix cores and the vector operations beside them. A workgroup
-// of 2 x 2 waves computes 128 rows by 128 columns of the packed order, a wave
+// of 2 x WN waves computes 128 rows by 64 WN columns of the packed order, a wave
 // 64 x 64 of them (4 x 4 blocks of 16 x 16). K advances by a block of 128: the
 // rows of x come straight to LDS (two stages, 32 KiB each, the next one on its
 // way while this one is multiplied), swizzled so that the 16 rows of an operand
@@ -22,7 +22,9 @@
 // come from k_w4_prepare, which also makes aligned rows of what is not: K padded
 // to whole blocks, fp32 as three bf16 pieces one behind the other.
 //
-// 4096 rows of 4096 x 4096 in bf16: 156 us, 881 TFLOP/s; 16384 rows of 16 gated
+// Copies of x are a fifth of the time (without them 128 x 128 tiles took 135 us
+// where it was 163 with them): WN is 4 where there are that many tiles, and 2 below.
+// 4096 rows of 4096 x 4096 in bf16: 151 us, 910 TFLOP/s; 16384 rows of 16 gated
 // experts of 4096 x 4096: 572 us, 960; a large product of bf16 matrices by the
 // library reaches 1116 (4096^3) to 1255 (8192^3). Wave tiles of 48 x 64, which
 // leave 40 registers over, 198 and 645 us.
@@ -98,13 +100,16 @@ struct W4TileArgs {
 };
 
 // G: the rows of x are looked up in row_index. ST: the scales' type.
-template <int T, int S, int ST, bool G>
-__global__ void __launch_bounds__(256, 2) k_w4_tile(W4TileArgs A) {
+template <int T, int WN, int S, int ST, bool G>
+__global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
     using O = W4Op<T>;
-    constexpr int WN = 2, P = O::P, NW = 2 * WN, CPW = kW4TileRows / 4 / NW;  // waves, copies a wave and stage
+    constexpr int P = O::P, NW = 2 * WN, CPW = kW4TileRows / 4 / NW;  // waves, copies a wave and stage
     constexpr int SB = ST == DQ_F32 ? 4 : 2, SW = (S * SB + 3) / 4;  // words of a column's scales
     __shared__ __attribute__((aligned(16))) char st0[kW4TileRows * 256];
     __shared__ __attribute__((aligned(16))) char st1[kW4TileRows * 256];
+    // with the stages 16 KiB for each wave's results at the end
+    constexpr int kMore = NW * 16 * kW4TileM * 256 - 2 * kW4TileRows * 256;
+    __shared__ __attribute__((aligned(16))) char st2[kMore > 0 ? kMore : 16];
     __shared__ __attribute__((aligned(16))) float s_sum[2][S][kW4TileRows];
     __shared__ int s_bad[kW4TileRows];
     const W4Args& a = A.a;
@@ -361,9 +366,8 @@ __global__ void __launch_bounds__(256, 2) k_w4_tile(W4TileArgs A) {
 
     // bias and gate, through this wave's part of the stages 
     // so that whole rows go out, 16 bytes a lane
-    constexpr int kPart = 2 * kW4TileRows * 256 / NW, kRows = 16 * kW4TileM;
-    static_assert(kPart >= kRows * 256, "a wave's rows of 64 in fp32");
-    char* part_base = wave < NW / 2 ? st0 + wave * kPart : st1 + (wave - NW / 2) * kPart;
+    constexpr int kRows = 16 * kW4TileM, kPart = kRows * 256, kIn = kW4TileRows * 256 / kPart;
+    char* part_base = wave < kIn ? st0 + wave * kPart : wave < 2 * kIn ? st1 + (wave - kIn) * kPart : st2 + (wave - 2 * kIn) * kPart;
     float* part = reinterpret_cast<float*>(part_base);
     const int cols = a.gated ? 32 : 64;
     const int n0 = (a.gated ? nt0 / 2 : nt0) * 16;
@@ -417,21 +421,25 @@ __global__ void __launch_bounds__(256, 2) k_w4_tile(W4TileArgs A) {
 // the instances for one type of x
 typedef void (*W4TileKernel)(W4TileArgs);
 typedef void (*W4PrepareKernel)(W4Prepare);
-template <int T, int S, int ST>
+template <int T, int WN, int S, int ST>
 W4TileKernel w4_tile_pick(bool gather) {
-    return gather ? k_w4_tile<T, S, ST, true> : k_w4_tile<T, S, ST, false>;
+    return gather ? k_w4_tile<T, WN, S, ST, true> : k_w4_tile<T, WN, S, ST, false>;
 }
-template <int T, int S>
+template <int T, int WN, int S>
 W4TileKernel w4_tile_pick(int scales, bool g) {
-    return scales == DQ_F32    ? w4_tile_pick<T, S, DQ_F32>(g)
-           : scales == DQ_BF16 ? w4_tile_pick<T, S, DQ_BF16>(g)
-                               : w4_tile_pick<T, S, DQ_F16>(g);
+    return scales == DQ_F32    ? w4_tile_pick<T, WN, S, DQ_F32>(g)
+           : scales == DQ_BF16 ? w4_tile_pick<T, WN, S, DQ_BF16>(g)
+                               : w4_tile_pick<T, WN, S, DQ_F16>(g);
+}
+template <int T, int WN>
+W4TileKernel w4_tile_pick(int S, int scales, bool g) {
+    return S == 4   ? w4_tile_pick<T, WN, 4>(scales, g)
+           : S == 2 ? w4_tile_pick<T, WN, 2>(scales, g)
+                    : w4_tile_pick<T, WN, 1>(scales, g);
 }
 template <int T>
-W4TileKernel w4_tile_pick(int S, int scales, bool gather) {
-    return S == 4   ? w4_tile_pick<T, 4>(scales, gather)
-           : S == 2 ? w4_tile_pick<T, 2>(scales, gather)
-                    : w4_tile_pick<T, 1>(scales, gather);
+W4TileKernel w4_tile_pick(int WN, int S, int scales, bool gather) {
+    return WN == 4 ? w4_tile_pick<T, 4>(S, scales, gather) : w4_tile_pick<T, 2>(S, scales, gather);
 }
 
 }  // namespace dq

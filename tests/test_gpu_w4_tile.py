@@ -61,9 +61,11 @@ KINDS = [("bf16", "bf16", "bf16", 128, True, True, False), ("bf16", "f32", "f32"
 
 
 @pytest.mark.parametrize("type,scale,y,group,zeros,bias,gated", KINDS)
-@pytest.mark.parametrize("rows,N,K", [(1100, 3100, 256), (1025, 2818, 392), (2049, 1600, 130)])
+@pytest.mark.parametrize("rows,N,K", [(1100, 3100, 256), (1025, 2818, 392), (2049, 1600, 130), (4225, 2100, 256),
+                                      (2177, 4130, 200)])
 def test_forward(gpu, type, scale, y, group, zeros, bias, gated, rows, N, K):
-    """Whole blocks of K, a K that ends inside one, rows that are copied first."""
+    """Whole blocks of K, a K that ends inside one, rows that are copied first;
+    the last two with a workgroup of 256 columns for every compute unit."""
     import torch
 
     N = N // 2 if gated else N
@@ -96,11 +98,16 @@ def test_grouped(gpu, type, gather):
     rows before and behind theirs are left."""
     import torch
 
-    counts, lead, tail = [0, 300, 1, 128, 129, 0, 255, 90], 5, 40
+    for counts, lead, tail, sizes in (([0, 300, 1, 128, 129, 0, 255, 90], 5, 40, (3400, 1700)),
+                                      ([700, 1, 0, 513, 900], 3, 30, (4400, 2200))):
+        _grouped_case(gpu, torch, type, gather, counts, lead, tail, sizes)
+
+
+def _grouped_case(gpu, torch, type, gather, counts, lead, tail, sizes):
     rows = lead + sum(counts) + tail
     offsets = [lead + sum(counts[:i]) for i in range(len(counts) + 1)]
     r = np.random.default_rng(3)
-    for gated, N, K, x_rows in ((False, 3400, 256, 77), (True, 1700, 200, 2 * rows)):
+    for gated, N, K, x_rows in ((False, sizes[0], 256, 77), (True, sizes[1], 200, 2 * rows)):
         idx = r.integers(0, x_rows, rows).tolist() if gather else None
         c = W.make(torch, K, len(counts), N, K, 64, x_rows if gather else rows, type, "bf16", not gated, gated, gated)
         log(f"w4 tiles grouped {type} gather {gather} gated {gated}")
