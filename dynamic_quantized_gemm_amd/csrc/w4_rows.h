@@ -89,10 +89,11 @@ __global__ void __launch_bounds__((w4_rows_waves<T, RT, CT, V>() * 64)) k_w4_row
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             w4_words<S * SB>(scales + ((size_t)j * A.blocks + b) * (16 * S * SB) + scale_at, k.scale[j]);
-            const int z = (j * A.blocks + b) * (16 * S);
-            if constexpr (S == 4) k.zero[j] = __builtin_amdgcn_raw_buffer_load_b32(zbuf, c * S, z, 0);
-            else if constexpr (S == 2) k.zero[j] = __builtin_amdgcn_raw_buffer_load_b16(zbuf, c * S, z, 0);
-            else k.zero[j] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, c * S, z, 0);
+            // all of the offset in the lane's part, which is what the buffer's size is held against
+            const int z = (j * A.blocks + b) * (16 * S) + c * S;
+            if constexpr (S == 4) k.zero[j] = __builtin_amdgcn_raw_buffer_load_b32(zbuf, z, 0, 0);
+            else if constexpr (S == 2) k.zero[j] = __builtin_amdgcn_raw_buffer_load_b16(zbuf, z, 0, 0);
+            else k.zero[j] = __builtin_amdgcn_raw_buffer_load_b8(zbuf, z, 0, 0);
         }
     };
     // The blocks in registers: one is multiplied, the others are on their way.
