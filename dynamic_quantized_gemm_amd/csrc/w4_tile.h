@@ -128,39 +128,34 @@ __global__ void __launch_bounds__(2 * WN * 64, 2) k_w4_tile(W4TileArgs A) {
     if (tile.first >= tile.end) return;
 
     // Copies of x: each takes 4 rows of 256 bytes, lane l the 16-byte piece (l %
-    // 16) ^ (row % 16) of row l / 16, to LDS in the order of the lanes. Without an
-    // index the rows of copies i and i + 4 differ by a distance alone.
+    // 16) ^ (row % 16) of row l / 16, to LDS in the order of the lanes. Rows past the
+    // tile's end repeat its last one (their results are not stored), one that does not
+    // exist the first of x (its result is NaN): every copy lies inside x.
     const int last = tile.end - 1;
-    constexpr int NV = G ? CPW : 4;
-    static_assert(CPW * NW * 4 == kW4TileRows, "every wave copies the same rows");
-    uint32_t voff[NV];
+    uint32_t voff[CPW];
     const int row0 = G ? 0 : tile.first - (A.x_by_row ? A.row_lo : 0);
     const uint32_t x_bytes = (uint32_t)(a.x_stride * 2);
     const int rows_here = tile.end - tile.first;
-    // ends with the last row: one past the tile's end reads as zeros, or as a row that is there
-    const uint32_t x_end = (uint32_t)((G ? a.x_rows : rows_here) - 1) * x_bytes + (uint32_t)(P * a.blocks) * (kW4Block * 2);
     __amdgpu_buffer_rsrc_t xbuf = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(static_cast<const char*>(a.x) + (long long)row0 * a.x_stride * 2), 0, (int)x_end, 0x00027000);
+        const_cast<char*>(static_cast<const char*>(a.x) + (long long)row0 * a.x_stride * 2), 0, -1, 0x00027000);
 #pragma unroll
     for (int i = 0; i < CPW; ++i) {
         const int r = (wave * CPW + i) * 4 + quad;
         int src = min(r, rows_here - 1);
+        bool bad = false;
         if (a.row_index) {
             const int at = a.row_index[tile.first + src];
-            const bool bad = at < 0 || at >= a.x_rows;
+            bad = at < 0 || at >= a.x_rows;
             if (G) src = bad ? 0 : at;
-            if (c == 0) s_bad[r] = bad;
-        } else if (c == 0) {
-            s_bad[r] = false;
         }
-        if (i < NV) voff[i] = (uint32_t)(G ? src : r) * x_bytes + (uint32_t)((c ^ (r & 15)) * 16);
+        if (c == 0) s_bad[r] = bad;
+        voff[i] = (uint32_t)src * x_bytes + (uint32_t)((c ^ (r & 15)) * 16);
     }
     auto copy = [&](int stage_k, char* dst) {
         // stage_k: the element of a row at which the stage's 128 begin
 #pragma unroll
         for (int i = 0; i < CPW; ++i)
-            buffer16_to_lds(xbuf, dst + (wave * CPW + i) * 1024, voff[i % NV],
-                            (uint32_t)stage_k * 2 + (uint32_t)(i / NV * 16) * x_bytes);
+            buffer16_to_lds(xbuf, dst + (wave * CPW + i) * 1024, voff[i], (uint32_t)stage_k * 2);
     };
     // the sums of x of thread t's row, as an offset (they take less than 2^32 bytes)
     uint32_t sum_at;
