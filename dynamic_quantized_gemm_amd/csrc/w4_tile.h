@@ -24,8 +24,8 @@
 //
 // Copies of x are a fifth of the time (without them 128 x 128 tiles took 135 us
 // where it was 163 with them): WN is 4 where there are that many tiles, and 2 below.
-// 4096 rows of 4096 x 4096 in bf16: 151 us, 910 TFLOP/s; 16384 rows of 16 gated
-// experts of 4096 x 4096: 572 us, 960; a large product of bf16 matrices by the
+// 4096 rows of 4096 x 4096 in bf16: 151 to 163 us by the card, 910 TFLOP/s at best; 16384 rows of 16 gated
+// experts of 4096 x 4096: 560 to 608 us, 980; a large product of bf16 matrices by the
 // library reaches 1116 (4096^3) to 1255 (8192^3). Wave tiles of 48 x 64, which
 // leave 40 registers over, 198 and 645 us.
 #pragma once
